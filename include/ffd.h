@@ -420,6 +420,158 @@ int32_t ffd_abi_version(void);
  * launched).  Use a buffer well above the 126 MB L2 to measure HBM. */
 ffd_status ffd_read_probe(const void *buf, size_t bytes, uint32_t *sink, void *cuda_stream);
 
+/* ---- Several new tokens a sequence: rotary positions, the cache write, an
+ * ---- 8-bit cache, and attention of drafted tokens over the cache ----
+ * The calls around the decode step when it takes more than one token, as in
+ * verifying a tree of drafted tokens: ffd_append_tokens rotates the new
+ * queries and keys and writes the new K/V rows, ffd_decode_tree attends from
+ * every drafted token.  With one token they are an ordinary dense step, and
+ * on an 8-bit cache the step that reads half the bytes.  They use of a shape
+ * the batch, heads, head dim and capacity (block_size and split_blocks are
+ * checked as everywhere but do not matter).
+ *
+ * Rotary positions.  Pair i of a head's first rotary_dim channels (channels i
+ * and i + rotary_dim / 2 in FFD_ROPE_HALF, 2i and 2i + 1 in
+ * FFD_ROPE_INTERLEAVED) is rotated by position * f_i and multiplied by
+ * `amplitude`; the other channels are copied.  f_i = base^(-2i / rotary_dim),
+ * scaled for long contexts by `scaling`:
+ *   FFD_ROPE_SCALE_NONE      f_i
+ *   FFD_ROPE_SCALE_LINEAR    f_i / factor (position interpolation)
+ *   FFD_ROPE_SCALE_BASE      base * factor^(rotary_dim / (rotary_dim - 2)) in
+ *                            place of base (nothing at rotary_dim 2)
+ *   FFD_ROPE_SCALE_BY_PARTS  with r = original_length * f_i / (2 pi) rotations
+ *                            over the trained length and g = clamp((r - low) /
+ *                            (high - low), 0, 1): (1 - g) f_i / factor + g f_i
+ * Angles are exact to 2^-32 of a turn at any 32-bit position, negative ones
+ * included: the frequency is held in turns as a 64-bit binary fraction, so the
+ * product with the position wraps at whole turns. */
+#define FFD_ROPE_HALF 0
+#define FFD_ROPE_INTERLEAVED 1
+#define FFD_ROPE_SCALE_NONE 0
+#define FFD_ROPE_SCALE_LINEAR 1
+#define FFD_ROPE_SCALE_BASE 2
+#define FFD_ROPE_SCALE_BY_PARTS 3
+
+typedef struct {
+  int32_t rotary_dim;     /* even, 2 .. 128 */
+  int32_t layout;         /* FFD_ROPE_HALF or FFD_ROPE_INTERLEAVED */
+  int32_t scaling;        /* FFD_ROPE_SCALE_* */
+  int32_t reserved;       /* 0 */
+  double base;            /* > 0 */
+  double factor;          /* > 0; ignored without scaling */
+  double original_length; /* > 0, by parts only */
+  double low, high;       /* 0 <= low < high, by parts only */
+  double amplitude;       /* > 0 */
+} ffd_rope_options;
+
+/* A rotary plan: host memory, filled by ffd_rope_init and read by the calls
+ * below before they return. */
+typedef struct {
+  uint64_t turns[64];     /* per pair: f_i / (2 pi) as a 64-bit binary fraction */
+  float amplitude;
+  int32_t rotary_dim, layout, reserved;
+} ffd_rope;
+
+ffd_status ffd_rope_init(const ffd_rope_options *options, ffd_rope *rope);
+
+/* Rotate bf16 [tokens][heads][128] queries and, with k_bf16 not NULL, keys in
+ * one launch; positions: int32 [tokens] on the device.  inverse == 1 turns by
+ * the opposite angle: the gradient of the call with 0 (and its inverse where
+ * the amplitude is 1).  Products and sums in fp32, rounded once.  An output
+ * may be its input; other overlaps of an output are rejected.  0 <= tokens <
+ * 2^31; heads in [1, 65535] (num_k_heads is ignored without k_bf16). */
+ffd_status ffd_rotate(const ffd_rope *rope, int64_t tokens, const int32_t *d_positions,
+                      int32_t inverse, int32_t num_q_heads, const void *q_bf16, void *q_out_bf16,
+                      int32_t num_k_heads, const void *k_bf16, void *k_out_bf16,
+                      void *cuda_stream);
+
+/* A KV cache in one of two formats.
+ *   FFD_CACHE_BF16: k, v bf16 [B][Hkv][cap][D]; the scale pointers are unused
+ *     (the cache of ffd_decode).
+ *   FFD_CACHE_BYTE: k, v e4m3 [B][Hkv][cap][D], k_scales, v_scales bf16
+ *     [B][Hkv][cap]: one scale a row.  Row x (fp32) is held as
+ *       amax = max_c |x_c|,  s = bf16_rne(amax / 448)   (IEEE fp32 division)
+ *       code_c = s == 0 ? 0 : e4m3_rne(x_c / s), clamped to +-448
+ *     and stands for code_c * s.  A row with an infinity or NaN in it gets a
+ *     NaN scale and NaN codes: it reads back as NaN throughout. */
+#define FFD_CACHE_BF16 0
+#define FFD_CACHE_BYTE 1
+
+typedef struct {
+  int32_t format;
+  int32_t reserved; /* 0 */
+  void *k, *v;
+  void *k_scales, *v_scales;
+} ffd_cache;
+
+/* Write new_tokens rows a sequence into the cache, and rotate.
+ *   q [B][new_tokens][Hq][D], k_new, v_new [B][new_tokens][Hkv][D] (bf16);
+ *   q_out as q, or q == q_out == NULL to leave the queries out;
+ *   rope NULL: nothing is rotated (q is then copied);
+ *   d_lengths int32 [B]: tokens per sequence, the new ones counted;
+ *   d_new_lengths int32 [B] or NULL: new tokens of each sequence, 0 ..
+ *     new_tokens (NULL: new_tokens in every one);
+ *   d_positions int32 [B][new_tokens] or NULL: the rotary positions (NULL:
+ *     each token's slot).
+ * Token i of sequence b goes to slot lengths[b] - count + i, k rotated in fp32
+ * and rounded (or quantised) once.  Rows i >= count of q_out and every other
+ * row of the cache are left as they were.  A sequence whose length is outside
+ * [0, cap], or whose count is outside [0, min(new_tokens, length)], is left
+ * out (ffd_decode_tree reports it).  q_out may be q; other overlaps between
+ * inputs and outputs are rejected. */
+ffd_status ffd_append_tokens(const ffd_shape *shape, const ffd_cache *cache, const ffd_rope *rope,
+                             int32_t new_tokens, const void *q_bf16, const void *k_new_bf16,
+                             const void *v_new_bf16, const int32_t *d_positions,
+                             const int32_t *d_lengths, const int32_t *d_new_lengths,
+                             void *q_out_bf16, void *cuda_stream);
+
+/* Read tokens token_begin .. token_begin + token_count - 1 of an
+ * FFD_CACHE_BYTE cache back to bf16: k_out, v_out [B][Hkv][token_count][D],
+ * code * scale rounded once (either may be NULL).  With token_begin 0 and
+ * token_count cap the outputs are a cache for ffd_quantize_keys and
+ * ffd_decode.  Rows of tokens at or past lengths[b] are left as they were, as
+ * is a sequence whose length is outside [0, cap].  0 <= token_begin,
+ * 0 <= token_count, token_begin + token_count <= cap. */
+ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const int32_t *d_lengths,
+                          int32_t token_begin, int32_t token_count, void *k_out_bf16,
+                          void *v_out_bf16, void *cuda_stream);
+
+/* Largest tree ffd_decode_tree takes. */
+#define FFD_MAX_TREE_NODES 64
+
+/* Attention of num_nodes drafted tokens a sequence over the cache, whose last
+ * rows hold them (ffd_append_tokens):
+ *   q, out bf16 [B][num_nodes][Hq][D];  d_lengths int32 [B], the tree counted;
+ *   d_tree_sizes int32 [B] or NULL: nodes of each sequence, 0 .. num_nodes
+ *     (NULL: num_nodes in every one);
+ *   d_tree_mask uint64 [B][num_nodes] or NULL: bit j of node i's word says
+ *     that node i sees node j.  A node sees itself only if its own bit is set,
+ *     and any set of nodes may be seen.  NULL: a chain (node i sees 0 .. i).
+ * With first = lengths[b] - size, node i of head h attends (softmax(q.K /
+ * sqrt(D)) V with the head's kv-head) over slots 0 .. first - 1 and the slots
+ * first + j it sees, j < size.  A node that sees nothing yields a zero row;
+ * what lies in unseen slots, NaN included, has no influence.  Rows i >= size
+ * of out are left as they were.  Scores, softmax statistics and sums are fp32;
+ * the softmax weights enter the product with V with 8 significant bits.
+ * A sequence whose length is outside [0, cap], or whose size is outside [0,
+ * min(num_nodes, length)], yields zero rows (all num_nodes) and sets
+ * FFD_DEVICE_FLAG_BAD_LENGTH in the workspace (ffd_check_device_status).
+ * 1 <= num_nodes <= FFD_MAX_TREE_NODES.  The result does not depend on what
+ * the workspace held.  Calls that share a workspace must not overlap on the
+ * GPU. */
+ffd_status ffd_decode_tree(const ffd_shape *shape, const ffd_cache *cache, int32_t num_nodes,
+                           const void *q_bf16, const int32_t *d_lengths,
+                           const int32_t *d_tree_sizes, const uint64_t *d_tree_mask,
+                           void *out_bf16, void *workspace, size_t workspace_bytes,
+                           void *cuda_stream);
+
+/* Bytes of that workspace (0 for an invalid shape or node count), and its
+ * first use: clear the error word. */
+size_t ffd_decode_tree_workspace_bytes(const ffd_shape *shape, int32_t num_nodes);
+ffd_status ffd_decode_tree_workspace_init(const ffd_shape *shape, int32_t num_nodes,
+                                          void *workspace, size_t workspace_bytes,
+                                          void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,8 @@ constexpr int32_t kAbiVersion = 2;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+}  // namespace
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 ffd_status check_shape(const ffd_shape *s) {
@@ -52,6 +54,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
 
 // K or V cache as a 3-D tensor {64 channels, token rows, 2 halves}: a row is
 // 128 bf16 (256 bytes) and a half its low or high 128 bytes.  One box

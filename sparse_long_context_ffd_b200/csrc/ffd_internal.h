@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -136,6 +137,11 @@ cudaError_t launch_decode(const DecodeParams &p, const CUtensorMap &tmap_k,
 }  // namespace ffd
 #include "ffd.h"
 namespace ffd {
+// Host checks and the tensor-map encoder, shared by the entry points.
+bool aligned16(const void *p);
+ffd_status check_shape(const ffd_shape *s);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // null without a driver
+
 ffd_status decode_shared_scratch(const ffd_shape *s, const void *q_bf16, const void *k_bf16,
                                  const void *v_bf16, const void *k_packed, const void *k_scales,
                                  const int32_t *d_lengths, float delta, void *out_bf16, uint32_t *mask,

@@ -1,0 +1,60 @@
+// ffd_serve.h -- parameter blocks and launchers of the multi-token operators:
+// rotary positions, the cache write, the 8-bit cache's read-back (rows.cu) and
+// attention of drafted tokens over the cache (tree.cu).
+#pragma once
+
+#include "ffd_internal.h"
+
+namespace ffd {
+
+constexpr int kMaxPairs = kHeadDim / 2;
+constexpr int kByteRow = kHeadDim;  // bytes of an e4m3 cache row
+
+// ffd_rotate and ffd_append_tokens.  A token's rows are its query heads, key
+// heads and (append only) value heads, in that order.
+struct RowsParams {
+  uint64_t turns[kMaxPairs];  // f / 2pi of each rotated pair, a 64-bit binary fraction
+  float amplitude, sign;      // sign -1: the opposite angle
+  int32_t rotary_dim, interleaved;
+  const uint16_t *q, *k, *v;    // null: no such rows
+  uint16_t *q_out;
+  void *k_out, *v_out;          // rotate: like the input; append: the cache
+  uint16_t *k_scales, *v_scales;
+  const int32_t *positions;     // null: the slot (append)
+  const int32_t *lengths, *counts;
+  int32_t tokens;               // rotate: tokens; append: batch * new_tokens
+  int32_t q_heads, kv_heads, new_tokens, capacity;
+};
+
+struct ReadParams {
+  const uint8_t *codes[2];      // k, v
+  const uint16_t *scales[2];
+  uint16_t *out[2];             // null: not wanted
+  const int32_t *lengths;
+  int32_t batch, kv_heads, capacity, begin, count;
+};
+
+// append: write k and v into the cache of the given format; else rotate only.
+cudaError_t launch_rows(const RowsParams &p, bool append, int format, cudaStream_t stream);
+cudaError_t launch_read(const ReadParams &p, cudaStream_t stream);
+
+struct TreeParams {
+  const uint16_t *q;            // bf16 [B][n][Hq][D]
+  const uint16_t *k_scales, *v_scales;
+  const uint8_t *k, *v;
+  const int32_t *lengths, *sizes;
+  const uint64_t *mask;
+  uint16_t *out;
+  uint32_t *err;
+  float *partials;
+  int32_t batch, kv_heads, group, nodes, capacity, format;
+};
+
+struct TreeLayout {
+  size_t partials, total;
+};
+
+TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t nodes);
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
+
+}  // namespace ffd

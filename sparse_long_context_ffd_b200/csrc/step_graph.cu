@@ -37,7 +37,6 @@ void destroy_parts(ffd_step_graph *g) {
   if (g->stream) cudaStreamDestroy(g->stream);
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 }  // namespace ffd

@@ -38,11 +38,19 @@ EXPORTED = (
     "ffd_decode_partials_tr", "ffd_decode_append", "ffd_decode_append_tr",
     "ffd_step_graph_create", "ffd_step_graph_run", "ffd_step_graph_destroy",
     "ffd_read_probe", "ffd_no_alloc_device_status",
+    "ffd_rope_init", "ffd_rotate", "ffd_append_tokens", "ffd_read_cache", "ffd_decode_tree",
+    "ffd_decode_tree_workspace_bytes", "ffd_decode_tree_workspace_init",
 )
 
 FFD_REFERENCE_RUNNING_MAX = 0
 FFD_REFERENCE_SINK_LOCAL = 1        # running maximum started at the sink/local pseudo-max
 FFD_REFERENCE_SINK_LOCAL_FIXED = 2  # the sink/local pseudo-max as a fixed threshold
+
+FFD_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+FFD_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+FFD_CACHE_BF16 = 0
+FFD_CACHE_BYTE = 1
+FFD_MAX_TREE_NODES = 64
 
 # Size of the library's built-in scratch array used by ffd_decode_no_alloc.
 FFD_NO_ALLOC_SCRATCH_BYTES = 16 << 20
@@ -67,6 +75,45 @@ class Shape(ctypes.Structure):
 
     def __repr__(self):
         return "Shape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class _RopeOptions(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    """A rotary plan (ffd_rope): made once from a model's settings, given to
+    rotate, append_tokens, StandInAttentionLayer and TreeStep.
+
+    layout: "half" (channels i and i + rotary_dim / 2 are a pair) or
+    "interleaved" (2i and 2i + 1); scaling: "none", "linear", "base" or
+    "by_parts" (the header has the formulas); by_parts takes original_length,
+    low and high."""
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("amplitude", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+    def __init__(self, rotary_dim: int = 128, layout: str = "half", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original_length: float = 0.0,
+                 low: float = 0.0, high: float = 0.0, amplitude: float = 1.0):
+        super().__init__()
+        if layout not in FFD_ROPE_LAYOUTS or scaling not in FFD_ROPE_SCALINGS:
+            raise ValueError("unknown rotary layout or scaling")
+        opts = _RopeOptions(int(rotary_dim), FFD_ROPE_LAYOUTS[layout], FFD_ROPE_SCALINGS[scaling], 0,
+                            float(base), float(factor), float(original_length), float(low),
+                            float(high), float(amplitude))
+        _check(load_library().ffd_rope_init(ctypes.byref(opts), ctypes.byref(self)),
+               "ffd_rope_init")
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
 def make_shape(batch, num_q_heads, num_kv_heads, capacity, block_size, split_blocks,
@@ -164,6 +211,17 @@ def load_library() -> ctypes.CDLL:
             lib.ffd_no_alloc_device_status.restype = st
             lib.ffd_check_device_status.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), p]
             lib.ffd_check_device_status.restype = st
+            lib.ffd_rope_init.argtypes = [ctypes.POINTER(_RopeOptions), ctypes.POINTER(Rope)]
+            lib.ffd_rotate.argtypes = [p, ctypes.c_int64, p, i32, i32, p, p, i32, p, p, p]
+            lib.ffd_append_tokens.argtypes = [sp, p, p, i32, p, p, p, p, p, p, p, p]
+            lib.ffd_read_cache.argtypes = [sp, p, p, i32, i32, p, p, p]
+            lib.ffd_decode_tree.argtypes = [sp, p, i32, p, p, p, p, p, p, sz, p]
+            lib.ffd_decode_tree_workspace_bytes.argtypes = [sp, i32]
+            lib.ffd_decode_tree_workspace_bytes.restype = sz
+            lib.ffd_decode_tree_workspace_init.argtypes = [sp, i32, p, sz, p]
+            for name in ("ffd_rope_init", "ffd_rotate", "ffd_append_tokens", "ffd_read_cache",
+                         "ffd_decode_tree", "ffd_decode_tree_workspace_init"):
+                getattr(lib, name).restype = st
             lib.ffd_read_probe.argtypes = [p, sz, p, p]
             lib.ffd_read_probe.restype = st
             lib.ffd_status_string.argtypes = [st]
@@ -406,6 +464,208 @@ def check_device_status(workspace, stream=None) -> int:
     if st not in (FFD_OK, FFD_ERR_DEVICE_CHECK, FFD_ERR_TIMEOUT):
         raise FFDError(st, "ffd_check_device_status")
     return int(flags.value)
+
+
+# ---- Several new tokens a sequence (rotary positions, cache writes, trees) ----
+# These wrappers check dtypes, shapes and devices before they pass pointers on,
+# and launch on the tensors' device: on its current stream unless one is given.
+
+
+def _tensor(t, dtype, shape, what: str, device: int) -> int:
+    """Data pointer of a dense CUDA tensor of exactly this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return t.data_ptr()
+
+
+def _device_of(t) -> int:
+    if not t.is_cuda:
+        raise ValueError("FFD entry points take CUDA tensors")
+    return t.get_device()
+
+
+def _call(device: int, stream, what: str, fn, *args) -> None:
+    """fn(*args, stream) with `device` current."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != FFD_OK:
+        raise FFDError(status, what)
+
+
+class KVCache:
+    """A KV cache of one layer: bf16 k and v [B, Hkv, cap, 128], or
+    float8_e4m3fn k and v with bf16 k_scales and v_scales [B, Hkv, cap] (one
+    scale a row).  Wraps the caller's tensors; `KVCache.empty` allocates."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        import torch
+        device = _device_of(k)
+        if k.dim() != 4 or k.shape[-1] != 128 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("k is bf16 or float8_e4m3fn [B, Hkv, cap, 128]")
+        self.format = FFD_CACHE_BF16 if k.dtype == torch.bfloat16 else FFD_CACHE_BYTE
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device, self.key = device, tuple(k.shape[:3])
+        if (self.format == FFD_CACHE_BYTE) != (k_scales is not None) or (k_scales is None) != (v_scales is None):
+            raise ValueError("an 8-bit cache has k_scales and v_scales, a bf16 cache has neither")
+        s = torch.Size(self.key)
+        self._c = _Cache(self.format, 0, _tensor(k, k.dtype, k.shape, "k", device),
+                         _tensor(v, k.dtype, k.shape, "v", device),
+                         None if k_scales is None else _tensor(k_scales, torch.bfloat16, s, "k_scales", device),
+                         None if v_scales is None else _tensor(v_scales, torch.bfloat16, s, "v_scales", device))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, shape: Shape, format: int = FFD_CACHE_BF16, device="cuda"):
+        import torch
+        key = (shape.batch, shape.num_kv_heads, shape.capacity)
+        if format == FFD_CACHE_BF16:
+            kv = [torch.empty((*key, 128), dtype=torch.bfloat16, device=device) for _ in range(2)]
+            return cls(*kv)
+        if format != FFD_CACHE_BYTE:
+            raise ValueError("unknown cache format")
+        kv = [torch.empty((*key, 128), dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+        return cls(*kv, *(torch.empty(key, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+    def _of(self, shape: Shape):
+        if self.key != (shape.batch, shape.num_kv_heads, shape.capacity):
+            raise ValueError(f"cache {self.key} does not fit {shape}")
+        return self._ref
+
+
+def rotate(rope: Rope, positions, q, q_out, k=None, k_out=None, inverse: bool = False,
+           stream=None) -> None:
+    """ffd_rotate: rotary positions of bf16 q [tokens, Hq, 128] and, if given,
+    k [tokens, Hkv, 128]; positions int32 [tokens].  An output may be its
+    input."""
+    import torch
+    dev, bf16 = _device_of(q), torch.bfloat16
+    if q.dim() != 3 or q.shape[2] != 128:
+        raise ValueError("q is [tokens, heads, 128]")
+    tokens = q.shape[0]
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    args = (ctypes.byref(rope), tokens, _tensor(positions, torch.int32, torch.Size((tokens,)), "positions", dev),
+            1 if inverse else 0, q.shape[1], _tensor(q, bf16, q.shape, "q", dev),
+            _tensor(q_out, bf16, q.shape, "q_out", dev))
+    if k is None:
+        args += (0, None, None)
+    else:
+        if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != 128:
+            raise ValueError("k is [tokens, heads, 128]")
+        args += (k.shape[1], _tensor(k, bf16, k.shape, "k", dev), _tensor(k_out, bf16, k.shape, "k_out", dev))
+    _call(dev, stream, "ffd_rotate", load_library().ffd_rotate, *args)
+
+
+def append_tokens(shape: Shape, cache: KVCache, k_new, v_new, lengths, rope: Optional[Rope] = None,
+                  positions=None, new_lengths=None, q=None, q_out=None, stream=None) -> None:
+    """ffd_append_tokens: rotate the new queries and keys (with `rope`) and
+    write the new K/V rows into the cache.  k_new, v_new bf16 [B, n, Hkv, 128];
+    q, q_out bf16 [B, n, Hq, 128] or neither; lengths int32 [B], the new tokens
+    counted; new_lengths int32 [B] for fewer than n; positions int32 [B, n]
+    (default: the slots)."""
+    import torch
+    dev, bf16, i32, size = cache.device, torch.bfloat16, torch.int32, torch.Size
+    B, n = shape.batch, k_new.shape[1]
+    kv = size((B, n, shape.num_kv_heads, 128))
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    qs = size((B, n, shape.num_q_heads, 128))
+    _call(dev, stream, "ffd_append_tokens", load_library().ffd_append_tokens, ctypes.byref(shape),
+          cache._of(shape), None if rope is None else ctypes.byref(rope), n,
+          None if q is None else _tensor(q, bf16, qs, "q", dev), _tensor(k_new, bf16, kv, "k_new", dev),
+          _tensor(v_new, bf16, kv, "v_new", dev),
+          None if positions is None else _tensor(positions, i32, size((B, n)), "positions", dev),
+          _tensor(lengths, i32, size((B,)), "lengths", dev),
+          None if new_lengths is None else _tensor(new_lengths, i32, size((B,)), "new_lengths", dev),
+          None if q_out is None else _tensor(q_out, bf16, qs, "q_out", dev))
+
+
+def read_cache(shape: Shape, cache: KVCache, lengths, token_begin: int, k_out=None, v_out=None,
+               stream=None) -> None:
+    """ffd_read_cache: tokens from token_begin on of an 8-bit cache back to
+    bf16; k_out, v_out [B, Hkv, count, 128], either may be None."""
+    import torch
+    if k_out is None and v_out is None:
+        raise ValueError("nothing to read: k_out and v_out are None")
+    count = (k_out if k_out is not None else v_out).shape[2]
+    want = torch.Size((shape.batch, shape.num_kv_heads, count, 128))
+    dev = cache.device
+    _call(dev, stream, "ffd_read_cache", load_library().ffd_read_cache, ctypes.byref(shape),
+          cache._of(shape), _tensor(lengths, torch.int32, torch.Size((shape.batch,)), "lengths", dev),
+          int(token_begin), count,
+          None if k_out is None else _tensor(k_out, torch.bfloat16, want, "k_out", dev),
+          None if v_out is None else _tensor(v_out, torch.bfloat16, want, "v_out", dev))
+
+
+def decode_tree_workspace_bytes(shape: Shape, num_nodes: int) -> int:
+    return int(load_library().ffd_decode_tree_workspace_bytes(ctypes.byref(shape), int(num_nodes)))
+
+
+def tree_workspace(shape: Shape, num_nodes: int, device="cuda"):
+    """A cleared workspace for decode_tree with up to num_nodes nodes."""
+    import torch
+    nbytes = decode_tree_workspace_bytes(shape, num_nodes)
+    if nbytes == 0:
+        raise ValueError(f"decode_tree does not take {shape} with {num_nodes} nodes")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _call(ws.get_device(), None, "ffd_decode_tree_workspace_init",
+          load_library().ffd_decode_tree_workspace_init, ctypes.byref(shape), int(num_nodes),
+          ws.data_ptr(), nbytes)
+    return ws
+
+
+def decode_tree(shape: Shape, cache: KVCache, q, lengths, out, workspace, tree_mask=None,
+                tree_sizes=None, stream=None) -> None:
+    """ffd_decode_tree: attention of n drafted tokens a sequence over the cache
+    that holds them in its last rows.  q, out bf16 [B, n, Hq, 128]; lengths
+    int32 [B], the tree counted; tree_mask int64 [B, n] (bit j of node i's
+    word: i sees j; default a chain); tree_sizes int32 [B] for fewer than n
+    nodes.  tree_from_parents makes masks from parent lists."""
+    import torch
+    dev, bf16, size = cache.device, torch.bfloat16, torch.Size
+    B, n = shape.batch, q.shape[1]
+    qs = size((B, n, shape.num_q_heads, 128))
+    _call(dev, stream, "ffd_decode_tree", load_library().ffd_decode_tree, ctypes.byref(shape),
+          cache._of(shape), n, _tensor(q, bf16, qs, "q", dev),
+          _tensor(lengths, torch.int32, size((B,)), "lengths", dev),
+          None if tree_sizes is None else _tensor(tree_sizes, torch.int32, size((B,)), "tree_sizes", dev),
+          None if tree_mask is None else _tensor(tree_mask, torch.int64, size((B, n)), "tree_mask", dev),
+          _tensor(out, bf16, qs, "out", dev),
+          _tensor(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel())
+
+
+def tree_from_parents(parents):
+    """(mask, depth) of trees given as parent lists: parents[b][i] is node i's
+    parent (an earlier node) or -1.  mask int64 [B, n]: each node sees its
+    ancestors and itself; depth int32 [B, n]: 0 at the roots, to be added to
+    the tree's first position.  Host tensors; shorter lists are padded with
+    nodes that see nothing."""
+    import torch
+    n = max((len(p) for p in parents), default=0)
+    if n > FFD_MAX_TREE_NODES:
+        raise ValueError(f"a tree has at most {FFD_MAX_TREE_NODES} nodes")
+    mask = torch.zeros((len(parents), n), dtype=torch.int64)
+    depth = torch.zeros((len(parents), n), dtype=torch.int32)
+    for b, tree in enumerate(parents):
+        words, depths = [], []
+        for i, parent in enumerate(tree):
+            if not -1 <= parent < i:
+                raise ValueError(f"node {i}: its parent is -1 or an earlier node, not {parent}")
+            words.append((words[parent] if parent >= 0 else 0) | 1 << i)
+            depths.append(depths[parent] + 1 if parent >= 0 else 0)
+            mask[b, i] = words[i] - (1 << 64) if words[i] >> 63 else words[i]
+            depth[b, i] = depths[i]
+    return mask, depth
 
 
 class DecodeBuffers:
