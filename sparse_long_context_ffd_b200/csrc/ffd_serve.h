@@ -38,6 +38,12 @@ struct ReadParams {
 cudaError_t launch_rows(const RowsParams &p, bool append, int format, cudaStream_t stream);
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream);
 
+constexpr int kTreeTile = 128;        // tokens of a tile
+constexpr int kTreeCtas = 148;        // one a multiprocessor
+constexpr int kTreeRows = 256;        // query rows of a unit: two accumulators of 128
+
+// A unit: up to kTreeRows query rows (node, head of the group) of one kv-head
+// of one sequence, over all the sequence's tiles.
 struct TreeParams {
   const uint16_t *q;            // bf16 [B][n][Hq][D]
   const uint16_t *k_scales, *v_scales;
@@ -46,15 +52,18 @@ struct TreeParams {
   const uint64_t *mask;
   uint16_t *out;
   uint32_t *err;
-  float *partials;
-  int32_t batch, kv_heads, group, nodes, capacity, format;
+  int2 *table;                  // [B][kv_heads][units a head]: first CTA * 2 + its slot, CTAs
+  float *partials;              // [ctas][2][rows][kPartialStride]
+  int32_t batch, kv_heads, group_log2, nodes, capacity, format;
+  int32_t units_a_head, rows, ctas;
 };
 
 struct TreeLayout {
-  size_t partials, total;
+  size_t table, partials, total;
+  int32_t units_a_head, rows, ctas;
 };
 
-TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t nodes);
+TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t nodes, int32_t capacity);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
 
 }  // namespace ffd

@@ -11,6 +11,8 @@ using namespace ffd;
 
 namespace {
 
+constexpr size_t kErrBytes = 256;  // the error word at the head of a workspace
+
 struct Range {
   const void *p;
   size_t bytes;
@@ -234,7 +236,7 @@ ffd_status ffd_read_cache(const ffd_shape *s, const ffd_cache *c, const int32_t 
 
 size_t ffd_decode_tree_workspace_bytes(const ffd_shape *s, int32_t num_nodes) {
   if (check_shape(s) != FFD_OK || num_nodes < 1 || num_nodes > FFD_MAX_TREE_NODES) return 0;
-  return tree_layout(s->batch, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, num_nodes).total;
+  return tree_layout(s->batch, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, num_nodes, s->capacity).total;
 }
 
 ffd_status ffd_decode_tree_workspace_init(const ffd_shape *s, int32_t num_nodes, void *workspace,
@@ -245,9 +247,8 @@ ffd_status ffd_decode_tree_workspace_init(const ffd_shape *s, int32_t num_nodes,
   if (workspace == nullptr || workspace_bytes < ffd_decode_tree_workspace_bytes(s, num_nodes))
     return FFD_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FFD_ERR_INVALID_ARG;
-  const size_t head = tree_layout(s->batch, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, num_nodes).partials;
-  return cudaMemsetAsync(workspace, 0, head, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? FFD_OK
-                                                                                                  : FFD_ERR_CUDA;
+  return cudaMemsetAsync(workspace, 0, kErrBytes, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? FFD_OK
+                                                                                                       : FFD_ERR_CUDA;
 }
 
 ffd_status ffd_decode_tree(const ffd_shape *s, const ffd_cache *c, int32_t num_nodes, const void *q_bf16,
@@ -258,7 +259,7 @@ ffd_status ffd_decode_tree(const ffd_shape *s, const ffd_cache *c, int32_t num_n
   if (num_nodes < 1 || num_nodes > FFD_MAX_TREE_NODES) return FFD_ERR_INVALID_ARG;
   if (s->batch == 0) return FFD_OK;
   const int group = s->num_q_heads / s->num_kv_heads;
-  const TreeLayout L = tree_layout(s->batch, s->num_kv_heads, group, num_nodes);
+  const TreeLayout L = tree_layout(s->batch, s->num_kv_heads, group, num_nodes, s->capacity);
   if (workspace == nullptr || workspace_bytes < L.total) return FFD_ERR_WORKSPACE;
   if (s->capacity > 0) {
     st = check_cache(c);
@@ -295,10 +296,14 @@ ffd_status ffd_decode_tree(const ffd_shape *s, const ffd_cache *c, int32_t num_n
   p.mask = d_tree_mask;
   p.out = static_cast<uint16_t *>(out_bf16);
   p.err = reinterpret_cast<uint32_t *>(ws);
+  p.table = reinterpret_cast<int2 *>(ws + L.table);
   p.partials = reinterpret_cast<float *>(ws + L.partials);
+  p.units_a_head = L.units_a_head;
+  p.rows = L.rows;
+  p.ctas = L.ctas;
   p.batch = s->batch;
   p.kv_heads = s->num_kv_heads;
-  p.group = group;
+  p.group_log2 = group == 8 ? 3 : group == 4 ? 2 : group == 2 ? 1 : 0;
   p.nodes = num_nodes;
   p.capacity = s->capacity;
   p.format = c->format;

@@ -1,100 +1,900 @@
-// tree.cu -- attention of drafted tokens over the cache: the plain kernel.
+// tree.cu -- attention of drafted tokens over the cache (ffd_decode_tree).
 //
-// One CTA of 128 threads per (node, query head, sequence).  128 tokens at a
-// time: thread t scores token t, the tile joins the running maximum and sum
-// (fp32), then thread c adds the tile's weighted values of channel c.
+// Query rows (node, head of the group) are the 128 lanes of a tensor-memory
+// accumulator, tokens its columns: S = Q K^T, P = 2^(S c - m), O += P V, one
+// pass over K and V with a running maximum m and sum l a row (fp32).  Few rows
+// are replicated over the lanes, a copy for each part of the tile's tokens, so
+// that every thread has work and no sum crosses lanes inside the pass.
+//
+// The work of a call is one list of 128-token tiles, (sequence, kv-head, rows)
+// after another, cut into equal parts, one for each CTA: long sequences are
+// split, short ones share a CTA, whatever the lengths are.  Parts of a unit
+// are joined by merge_kernel, in the order of the CTAs.
+//
+// A CTA: two groups of 128 softmax threads, one thread that issues the copies
+// and one that issues the matrix instructions.  Up to 128 rows, the groups
+// take alternate tiles with an accumulator each; more, they take 128 rows each
+// of the same tiles.  Either way the tensor cores work for one group while the
+// other does its exponentials.
+//
+// bf16 cache: P has bf16's 8 significant bits.  8-bit cache: codes enter the
+// matrix instructions as they are.  The query row, scaled by a power of two
+// into e4m3's range, is the sum of two e4m3 parts (exact for channels down to
+// 2^-9 of the row's largest, half of 2^-17 of it off below); the K row's scale
+// multiplies the score in fp32; the V row's scale multiplies the weight, which
+// is the sum of two e4m3 parts too: 8 significant bits, in units of 2^-16 of
+// the largest weight so far, or finer.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "ffd_ptx.cuh"
 #include "ffd_serve.h"
+#include "ffd_tcgen05.cuh"
 
 namespace ffd {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = kTreeTile;
+constexpr int kGroup = 128;                  // threads of a softmax group
+constexpr int kCtaThreads = 3 * kGroup;       // and four warps, of which one copies and one multiplies
+constexpr int kSmemMax = 232448;
+constexpr int kOutTile = 32768;               // bytes of a Q tile (bf16, or two e4m3 parts)
+constexpr float kScoreScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 
-__device__ __forceinline__ float e4m3_f(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half *>(&h));
+__device__ __forceinline__ float bf16_f(uint32_t b) { return __uint_as_float(b << 16); }
+
+__device__ __forceinline__ float exp2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ float bf16_f(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 
-template <bool kByte>
-__global__ void __launch_bounds__(kTile) tree_kernel(const TreeParams p) {
-  __shared__ float q_s[kHeadDim], w_s[kTile], red[4];
-  const int i = blockIdx.x, head = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
-  const int heads = p.kv_heads * p.group;
-  uint16_t *out = p.out + ((static_cast<size_t>(b) * p.nodes + i) * heads + head) * kHeadDim;
-  const int len = p.lengths[b], size = p.sizes != nullptr ? p.sizes[b] : p.nodes;
-  if (len < 0 || len > p.capacity || size < 0 || size > p.nodes || size > len) {
-    if (t == 0) atomicOr(p.err, kFlagBadLength);
-    out[t] = 0;
-    return;
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two fp16 values as e4m3 `hi` and, of what is left, e4m3 `lo`.
+__device__ __forceinline__ void split_e4m3(uint32_t pair, uint32_t &hi, uint32_t &lo) {
+  uint16_t h, l;
+  uint32_t back, rest;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(pair));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+  rest = sub_f16x2(pair, back);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
+  hi = h;
+  lo = l;
+}
+
+// ------------------------------------------------------------------- work --
+
+struct Sequence {
+  int len, size;
+  bool good;
+  __device__ __forceinline__ Sequence(const TreeParams &p, int b) {
+    len = p.lengths[b];
+    size = p.sizes != nullptr ? p.sizes[b] : p.nodes;
+    good = len >= 0 && len <= p.capacity && size >= 0 && size <= p.nodes && size <= len;
   }
-  if (i >= size) return;
-  const size_t row0 = (static_cast<size_t>(b) * p.kv_heads + head / p.group) * p.capacity;
-  const int first = len - size;
-  const uint64_t seen = p.mask != nullptr ? p.mask[static_cast<size_t>(b) * p.nodes + i] : (2ull << i) - 1ull;
-  q_s[t] = bf16_f(p.q[((static_cast<size_t>(b) * p.nodes + i) * heads + head) * kHeadDim + t]) *
-           (0.08838834764831845f * 1.4426950408889634f);
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int t0 = 0; t0 < len; t0 += kTile) {
+  // tiles of each of its units
+  __device__ __forceinline__ int tiles() const { return good && size > 0 ? (len + kTile - 1) / kTile : 0; }
+};
+
+struct Segment {
+  int b, unit, tile0, tiles, all;  // tiles of the unit in this CTA, and in all
+  int len, size;
+};
+
+// A CTA's part of the tile list, segment by segment.
+struct Walk {
+  int b, off, left;
+  __device__ __forceinline__ bool next(const TreeParams &p, Segment &g) {
+    if (left == 0) return false;
+    const int units = p.kv_heads * p.units_a_head;
+    for (; b < p.batch; ++b, off = 0) {
+      const Sequence q(p, b);
+      const int each = q.tiles();
+      if (off >= each * units) continue;
+      g.b = b;
+      g.unit = off / each;
+      g.tile0 = off - g.unit * each;
+      g.all = each;
+      g.tiles = min(each - g.tile0, left);
+      g.len = q.len;
+      g.size = q.size;
+      off += g.tiles;
+      left -= g.tiles;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------ layout --
+
+template <bool kByte, bool kPair>
+struct Layout {
+  static constexpr int kSlot = kByte ? 16384 : 32768;  // bytes of K or V of a tile
+  static constexpr int kQ = (kPair ? 2 : 1) * kOutTile;
+  static constexpr int kSlots = kByte ? (kPair ? 8 : 10) : (kPair ? 5 : 6);
+  static constexpr int kRing = kQ;
+  static constexpr int kScales = kRing + kSlots * kSlot;               // [slot][K, V][128] bf16
+  static constexpr int kTokens = kScales + (kByte ? kSlots * 512 : 0);  // [group][2][3][128] fp32
+  static constexpr int kRow = kTokens + (kByte ? 2 * 2 * 3 * 512 : 0);  // [2][128] float2
+  static constexpr int kBars = kRow + 2 * kGroup * 8;
+  static constexpr int kNumBars = 2 * kSlots + 8;
+  static constexpr int kWords = kBars + kNumBars * 8;
+  static constexpr int kTotal = kWords + 32;
+  static_assert(kTotal <= kSmemMax, "shared memory");
+};
+
+// --------------------------------------------------------------- the kernel --
+
+template <bool kByte, int kCols, bool kPair>
+__global__ void __launch_bounds__(kCtaThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                const TreeParams p) {
+  using L = Layout<kByte, kPair>;
+  constexpr int kRep = kTile / kCols;        // copies of a row
+  constexpr int kRowsHere = kGroup / kRep;   // rows of an accumulator
+  constexpr int kSlots = L::kSlots;
+  constexpr uint32_t kIdescS = instr_desc(kByte ? 0 : 1, false), kIdescO = instr_desc(kByte ? 0 : 1, true);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  float2 *row_s = reinterpret_cast<float2 *>(smem + L::kRow);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
+  uint64_t *full = bars, *empty = bars + kSlots;
+  uint64_t *bar_s = bars + 2 * kSlots, *bar_p = bar_s + 2, *bar_o = bar_s + 4, *bar_q = bar_s + 6;
+  uint64_t *bar_end = bar_s + 7;
+  volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
+  volatile int *dead = words + 1;      // a wait ran out
+  volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
+  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_s + s, 1);
+      mbar_init(bar_p + s, kGroup);
+      mbar_init(bar_o + s, 1);
+    }
+    mbar_init(bar_q, 2 * kGroup);
+    mbar_init(bar_end, 1);
+    fence_mbar_init();
+    *dead = 0;
+    *odd = 0;
+    start_s[0] = start_s[1] = start_s[2] = 0;
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  {  // this CTA's part of the tiles: thread t adds up the sequences of its chunk
+    int *sum_s = reinterpret_cast<int *>(row_s);
+    const int chunk = (p.batch + kCtaThreads - 1) / kCtaThreads;
+    const int b0 = min(p.batch, tid * chunk), b1 = min(p.batch, b0 + chunk);
+    const int units = p.kv_heads * p.units_a_head;
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += Sequence(p, b).tiles() * units;
+    int upto = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int other = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if ((tid & 31) >= d) upto += other;
+    }
+    if ((tid & 31) == 31) sum_s[warp] = upto;
     __syncthreads();
-    const int token = t0 + t;
-    const bool see = token < first || (token < len && ((seen >> (token - first)) & 1ull));
-    float s = -INFINITY;
-    if (see) {
-      s = 0.0f;
-      if (kByte) {
-        const uint8_t *k = p.k + (row0 + token) * kByteRow;
-        for (int c = 0; c < kHeadDim; ++c) s += q_s[c] * e4m3_f(k[c]);
-        s *= bf16_f(p.k_scales[row0 + token]);
-      } else {
-        const uint16_t *k = reinterpret_cast<const uint16_t *>(p.k) + (row0 + token) * kHeadDim;
-        for (int c = 0; c < kHeadDim; ++c) s += q_s[c] * bf16_f(k[c]);
+    int total = 0, before = upto - sum;
+    for (int w = 0; w < kCtaThreads / 32; ++w) {
+      if (w < warp) before += sum_s[w];
+      total += sum_s[w];
+    }
+    const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
+    int begin = 0, end = 0;
+    if (static_cast<int>(blockIdx.x) < ctas) {
+      begin = static_cast<int>(static_cast<int64_t>(blockIdx.x) * total / ctas);
+      end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / ctas);
+    }
+    if (begin >= before && begin < before + sum && end > begin) {
+      int off = begin - before, b = b0;
+      for (; b < b1; ++b) {
+        const int n = Sequence(p, b).tiles() * units;
+        if (off < n) break;
+        off -= n;
+      }
+      start_s[0] = b;
+      start_s[1] = off;
+      start_s[2] = end - begin;
+    }
+    if (tid == 0) start_s[3] = total;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tmem = static_cast<uint32_t>(words[0]);
+  Walk walk{start_s[0], start_s[1], start_s[2]};
+  Segment g;
+
+  // sticky: after one wait ran out nobody waits, loads or multiplies any more
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*dead) return false;
+      if ((i & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+        *dead = 1;
+        atomicOr(p.err, kFlagTimeout);
+        return false;
       }
     }
-    float top = s;
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if ((t & 31) == 0) red[t >> 5] = top;
-    __syncthreads();
-    const float m_new = fmaxf(fmaxf(m, fmaxf(red[0], red[1])), fmaxf(red[2], red[3]));
-    const float ref = m_new == -INFINITY ? 0.0f : m_new;
-    const float w = see ? exp2f(s - ref) : 0.0f;
-    w_s[t] = w;
-    const float fade = exp2f(m - ref);
-    m = m_new;
-    o *= fade;
-    l *= fade;
-    __syncthreads();
-    const int n = min(kTile, len - t0);
-    for (int j = 0; j < n; ++j) {
-      const int tok = t0 + j;
-      if (tok >= first && !((seen >> (tok - first)) & 1ull)) continue;
-      l += w_s[j];
-      const float v = kByte ? e4m3_f(p.v[(row0 + tok) * kByteRow + t]) * bf16_f(p.v_scales[row0 + tok])
-                            : bf16_f(reinterpret_cast<const uint16_t *>(p.v)[(row0 + tok) * kHeadDim + t]);
-      o += w_s[j] * v;
+  };
+
+  // Registers move from the last four warps to the softmax groups: 2 x 128 x
+  // 208 + 128 x 88 are the 384 x 168 that the CTA starts with.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+    // ------------------------------------------------------------- copies --
+    if ((tid & 31) == 0) {
+      uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
+      bool alive = true;
+      while (alive && walk.next(p, g)) {
+        const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
+        for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
+          const uint32_t slot = i % kSlots, round = i / kSlots;
+          if (round > 0 && !wait(empty + slot, (round - 1) & 1)) {
+            alive = false;
+            break;
+          }
+          const int t0 = (g.tile0 + (j >> 1)) * kTile;
+          const int row = bh * p.capacity + t0;
+          uint8_t *dst = smem + L::kRing + slot * L::kSlot;
+          const void *map = (j & 1) ? &tmap_v : &tmap_k;
+          if constexpr (kByte) {
+            const uint32_t scale_bytes = 2u * static_cast<uint32_t>(min(kTile, p.capacity - t0));
+            mbar_arrive_expect_tx(full + slot, L::kSlot + ((j & 1) ? 2 * scale_bytes : 0));
+            tma_load_2d(dst, map, 0, row, full + slot);
+            if (j & 1) {
+              bulk_g2s(smem + L::kScales + slot * 512, p.k_scales + row, scale_bytes, full + slot);
+              bulk_g2s(smem + L::kScales + slot * 512 + 256, p.v_scales + row, scale_bytes, full + slot);
+            }
+          } else {
+            mbar_arrive_expect_tx(full + slot, L::kSlot);
+            tma_load_3d(dst, map, 0, row, 0, full + slot);
+          }
+        }
+      }
+      if (*dead)  // what is in flight lands before the CTA ends
+        for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
+          mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ matrices --
+    if ((tid & 31) == 0) {
+      uint32_t n = 0, segments = 0, p_count[2] = {0, 0};
+      const uint32_t smem0 = smem_addr(smem);
+      bool alive = true;
+      auto scores = [&](int s, int j) {
+        const uint32_t i = 2 * (n + j), slot = i % kSlots;
+        alive = alive && wait(full + slot, (i / kSlots) & 1);
+        if (!alive) return;
+        tc_fence_after();
+        const uint32_t q = smem0 + (kPair ? s * kOutTile : 0), k = smem0 + L::kRing + slot * L::kSlot;
+        const uint32_t d = tmem + 128 * s;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          // bf16: 16 channels a step, four steps a 128-byte half; e4m3: 32
+          // channels a step, the row's first part and then its second
+          const uint32_t a = q + (c >> 2) * 16384 + (c & 3) * 32;
+          const uint32_t b = k + (kByte ? 0 : (c >> 2) * 16384) + (c & 3) * 32;
+          mma_ss<kByte>(d, smem_desc(a), smem_desc(b), kIdescS, c > 0);
+        }
+        mma_commit(bar_s + s);
+        if (!kPair || s == 1) mma_commit(empty + slot);
+      };
+      auto values = [&](int s, int j, bool first) {
+        const uint32_t i = 2 * (n + j) + 1, slot = i % kSlots;
+        alive = alive && wait(bar_p + s, p_count[s] & 1) && wait(full + slot, (i / kSlots) & 1);
+        ++p_count[s];
+        if (!alive) return;
+        tc_fence_after();
+        const uint32_t a = tmem + 128 * s, v = smem0 + L::kRing + slot * L::kSlot, d = tmem + 256 + 128 * s;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          // bf16: 16 tokens a step; e4m3: 32 tokens, first parts, then second
+          const uint32_t b = v + (kByte ? (c & 3) * 4096 : c * 2048);
+          mma_ts<kByte>(d, a + 8 * c, smem_desc(b, 16384), kIdescO, !first || c > 0);
+        }
+        if (!kPair || s == 1) mma_commit(empty + slot);
+      };
+      while (alive && walk.next(p, g)) {
+        alive = wait(bar_q, segments & 1);
+        ++segments;
+        for (int j = 0; alive && j <= g.tiles; ++j) {
+          if constexpr (kPair) {
+            for (int s = 0; s < 2; ++s) {
+              if (j > 0) values(s, j - 1, j == 1);
+              if (j < g.tiles) scores(s, j);
+              else if (alive) mma_commit(bar_o + s);
+            }
+          } else {
+            if (j < g.tiles) scores(j & 1, j);
+            if (j > 0) {
+              values((j - 1) & 1, j - 1, j <= 2);
+              if (alive && j - 1 >= g.tiles - 2) mma_commit(bar_o + ((j - 1) & 1));
+            }
+          }
+        }
+        n += g.tiles;
+      }
+      if (*dead) {  // what was issued is done before tensor memory is given back
+        mma_commit(bar_end);
+        mbar_wait(bar_end, 0, kWaitLimitNs);
+      }
+    }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int s = warp >> 2;                     // group
+    const int t = tid & (kGroup - 1);            // lane of the accumulator
+    const int w = warp & 3;
+    const int row = t & (kRowsHere - 1);
+    const int part = t / kRowsHere;              // which tokens of a tile: kCols from part * kCols on
+    const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
+    const uint32_t tm_s = tmem + lanes + 128 * s, tm_o = tmem + lanes + 256 + 128 * s;
+    uint32_t s_count = 0, o_count = 0, n = 0;
+    bool starts = true;                          // the CTA's first segment
+    while (walk.next(p, g)) {
+      const int head = g.unit / p.units_a_head;
+      const int block = (g.unit - head * p.units_a_head) * kTreeRows + (kPair ? s * kGroup : 0);
+      const int first = g.len - g.size;
+      const int bh = g.b * p.kv_heads + head;
+      // ---- the query rows ----
+      const int qr = block + row, node = qr >> p.group_log2;
+      const bool live = node < g.size;
+      float score_scale = kScoreScale;
+      uint64_t seen = 0;
+      {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (((static_cast<size_t>(g.b) * p.nodes + (live ? node : 0)) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+            (qr & ((1 << p.group_log2) - 1)) * kHeadDim);
+        const uint64_t in_tree = g.size >= 64 ? ~0ull : (1ull << g.size) - 1ull;
+        if (live)
+          seen = (p.mask != nullptr ? p.mask[static_cast<size_t>(g.b) * p.nodes + node] : (2ull << node) - 1ull) & in_tree;
+        uint8_t *dst = smem + (kPair ? s * kOutTile : 0) + t * 128;
+        if constexpr (kByte) {
+          uint4 q[16];
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            q[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+          }
+          // largest magnitude into [128, 256): in e4m3's range with all its bits
+          const int exponent = min(100, top == 0 ? 0 : 7 - ilogbf(bf16_f(top)));
+          const float up = top < 0x7F80u ? ldexpf(1.0f, exponent) : 0.0f;
+          score_scale = top < 0x7F80u ? ldexpf(kScoreScale, -exponent) : __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 &y = q[2 * c + (e >> 1)];
+              const uint32_t a = (e & 1) ? y.z : y.x, b = (e & 1) ? y.w : y.y;
+              uint32_t h0, l0, h1, l1;
+              split_e4m3(pack_f16(bf16_f(a & 0xFFFFu) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
+              split_e4m3(pack_f16(bf16_f(b & 0xFFFFu) * up, __uint_as_float(b & 0xFFFF0000u) * up), h1, l1);
+              hi[e] = h0 | h1 << 16;
+              lo[e] = l0 | l1 << 16;
+            }
+            const int at = (c ^ (t & 7)) << 4;
+            if (kPair || s == 0) *reinterpret_cast<uint4 *>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (kPair || s == 1) *reinterpret_cast<uint4 *>(dst + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (!kPair && (c >> 3) != s) continue;
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4)) =
+                live ? src[c] : make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar_q);
+
+      // ---- the tiles ----
+      float m = -INFINITY, l = 0.0f;
+      for (int j = kPair ? 0 : s; j < g.tiles; j += kPair ? 1 : 2) {
+        const int t0 = (g.tile0 + j) * kTile;
+        const bool masked = t0 + kTile > first;
+        const uint32_t vi = 2 * (n + j) + 1, v_slot = vi % kSlots;
+        const float4 *tok = nullptr;  // [3][kCols]: K scale, V scale, its log2
+        if constexpr (kByte) {
+          wait(full + v_slot, (vi / kSlots) & 1);
+          const uint16_t *raw = reinterpret_cast<const uint16_t *>(smem + L::kScales + v_slot * 512);
+          float *mine = reinterpret_cast<float *>(smem + L::kTokens) + (s * 2 + (s_count & 1)) * 3 * kTile;
+          const float vs = bf16_f(raw[kTile + t]);
+          mine[t] = bf16_f(raw[t]);
+          mine[kTile + t] = vs;
+          // (a zero scale: far below any other, but not infinitely far)
+          const float lv = log2f(fabsf(vs));
+          mine[2 * kTile + t] = lv < -60.0f ? -60.0f : lv;
+          named_barrier(2 + s, kGroup);
+          tok = reinterpret_cast<const float4 *>(mine + part * kCols);
+        }
+        wait(bar_s + s, s_count & 1);
+        ++s_count;
+        tc_fence_after();
+        float x[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) tmem_ld32(tm_s + part * kCols + c, x + c);
+        tmem_wait_ld32(x);
+#pragma unroll
+        for (int c = 32; c < kCols; c += 32) tmem_tie32(x + c);
+        if constexpr (kByte) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 ks = tok[c >> 2];
+            x[c] *= ks.x;
+            x[c + 1] *= ks.y;
+            x[c + 2] *= ks.z;
+            x[c + 3] *= ks.w;
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            const int at = t0 + part * kCols + c - first;  // the first column's node (below 0: before the tree)
+            uint32_t bits;
+            if (at <= -32)
+              bits = ~0u;
+            else if (at < 0)
+              bits = static_cast<uint32_t>(seen << -at) | ((1u << -at) - 1u);
+            else
+              bits = at < 64 ? static_cast<uint32_t>(seen >> at) : 0u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((bits >> e) & 1u)) x[c + e] = -INFINITY;
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (kByte) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 lv = tok[(2 * kTile + c) >> 2];
+            top[0] = fmaxf(top[0], fmaf(x[c], score_scale, lv.x));
+            top[1] = fmaxf(top[1], fmaf(x[c + 1], score_scale, lv.y));
+            top[2] = fmaxf(top[2], fmaf(x[c + 2], score_scale, lv.z));
+            top[3] = fmaxf(top[3], fmaf(x[c + 3], score_scale, lv.w));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+        }
+        float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // The reference m moves only when weights would leave their range: in
+        // bf16 past 2^8; in e4m3 past 448 (2^8.8), from 2^7 at the last move,
+        // so that small weights keep their bits.  O follows, which is idle:
+        // the product before the one that made S was the last to add to it.
+        constexpr float kRoom = kByte ? 8.8f : 8.0f;
+        if constexpr (kByte) high -= 7.0f; else high *= kScoreScale;
+        if (j < 2 && (kPair ? j == 0 : true)) {
+          m = high;
+        } else if (__any_sync(0xFFFFFFFFu, high > m + (kByte ? kRoom - 7.0f : kRoom))) {
+          const float next = fmaxf(m, high);
+          const float f = next == m ? 1.0f : exp2_f(m - next);
+          m = next;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            tmem_ld32(tm_o + c, o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st<32>(tm_o + c, reinterpret_cast<const uint32_t *>(o));
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (kByte) {
+          uint32_t hi[kCols / 4], lo[kCols / 4];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 vs = tok[(kTile + c) >> 2];
+            const float p0 = exp2_f(fmaf(x[c], score_scale, -ref)), p1 = exp2_f(fmaf(x[c + 1], score_scale, -ref));
+            const float p2 = exp2_f(fmaf(x[c + 2], score_scale, -ref)), p3 = exp2_f(fmaf(x[c + 3], score_scale, -ref));
+            sum[0] += p0;
+            sum[1] += p1;
+            sum[2] += p2;
+            sum[3] += p3;
+            // (an unseen token's scale may be anything)
+            const float w0 = masked && x[c] == -INFINITY ? 0.0f : p0 * vs.x;
+            const float w1 = masked && x[c + 1] == -INFINITY ? 0.0f : p1 * vs.y;
+            const float w2 = masked && x[c + 2] == -INFINITY ? 0.0f : p2 * vs.z;
+            const float w3 = masked && x[c + 3] == -INFINITY ? 0.0f : p3 * vs.w;
+            uint32_t h0, l0, h1, l1;
+            split_e4m3(pack_f16(w0, w1), h0, l0);
+            split_e4m3(pack_f16(w2, w3), h1, l1);
+            hi[c >> 2] = h0 | h1 << 16;
+            lo[c >> 2] = l0 | l1 << 16;
+          }
+          constexpr int kWide = kCols / 4;
+          uint32_t none[kWide];
+#pragma unroll
+          for (int c = 0; c < kWide; ++c) none[c] = 0u;
+#pragma unroll
+          for (int r = 0; r < kRep; ++r) {
+            if (r == part) {
+              tmem_st<kWide>(tm_s + r * kWide, hi);
+              tmem_st<kWide>(tm_s + 32 + r * kWide, lo);
+            } else {
+              tmem_st<kWide>(tm_s + r * kWide, none);
+              tmem_st<kWide>(tm_s + 32 + r * kWide, none);
+            }
+          }
+        } else {
+          uint32_t pairs[kCols / 2];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            const float p0 = exp2_f(fmaf(x[c], kScoreScale, -ref)), p1 = exp2_f(fmaf(x[c + 1], kScoreScale, -ref));
+            sum[c & 2] += p0;
+            sum[(c & 2) + 1] += p1;
+            pairs[c >> 1] = pack_bf16(p0, p1);
+          }
+          if constexpr (kRep == 1) {
+            tmem_st<32>(tm_s, pairs);
+            tmem_st<32>(tm_s + 32, pairs + 32);
+          } else {
+            constexpr int kWide = kCols / 2;
+            uint32_t none[kWide];
+#pragma unroll
+            for (int c = 0; c < kWide; ++c) none[c] = 0u;
+#pragma unroll
+            for (int r = 0; r < kRep; ++r) {
+              if (r == part) tmem_st<kWide>(tm_s + r * kWide, pairs);
+              else tmem_st<kWide>(tm_s + r * kWide, none);
+            }
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        if (masked) {
+          // A weight of zero must not meet a value that is not finite.  Rows
+          // past the sequence hold anything; a drafted token's row may hold
+          // infinities or NaN that some nodes see: they are taken out here and
+          // put back, for those nodes, at the end.
+          wait(full + v_slot, (vi / kSlots) & 1);
+          const int token = t0 + t;
+          if (token >= first) {
+            uint4 *v = reinterpret_cast<uint4 *>(smem + L::kRing + v_slot * L::kSlot + t * 128);
+            bool bad = false;
+            for (int c = 0; c < (kByte ? 8 : 16); ++c) {
+              uint4 &y = v[(c >> 3) * 1024 + ((c + t) & 7)];
+              if (token >= g.len) {
+                y = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint32_t x4[4] = {y.x, y.y, y.z, y.w};
+              bool changed = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (kByte) {
+#pragma unroll
+                  for (int h = 0; h < 32; h += 8)
+                    if (((x4[e] >> h) & 0x7Fu) == 0x7Fu) {
+                      x4[e] &= ~(0xFFu << h);
+                      changed = true;
+                    }
+                } else {
+#pragma unroll
+                  for (int h = 0; h < 32; h += 16)
+                    if (((x4[e] >> h) & 0x7F80u) == 0x7F80u) {
+                      x4[e] &= ~(0xFFFFu << h);
+                      changed = true;
+                    }
+                }
+              }
+              if (changed) {
+                y = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+                bad = true;
+              }
+            }
+            if (bad) *odd = 1;
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(bar_p + s);
+      }
+      n += g.tiles;
+
+      // ---- the end of a segment ----
+      const bool both = kPair || g.tiles > 1;  // both accumulators hold something
+      if (both || s == 0) {
+        wait(bar_o + s, o_count & 1);
+        ++o_count;
+      }
+      row_s[s * kGroup + t] = make_float2(m, l);
+      tc_fence_after();
+      named_barrier(1, 2 * kGroup);
+      const bool whole = g.tiles == g.all;
+      const bool any_odd = *odd != 0;
+      float f0 = 1.0f, f1 = 0.0f, row_m = m, row_l = l;
+      if constexpr (!kPair) {
+        row_m = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 2 * kRep; ++r)
+          row_m = fmaxf(row_m, row_s[(r & 1) * kGroup + (r >> 1) * kRowsHere + row].x);
+        const float ref = row_m == -INFINITY ? 0.0f : row_m;
+        row_l = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 2 * kRep; ++r) {
+          const float2 v = row_s[(r & 1) * kGroup + (r >> 1) * kRowsHere + row];
+          row_l += v.y * exp2_f(v.x - ref);
+        }
+        f0 = exp2_f(row_s[t].x - ref);
+        f1 = exp2_f(row_s[kGroup + t].x - ref);
+        named_barrier(1, 2 * kGroup);
+        row_s[s * kGroup + t] = make_float2(row_m, row_l);  // every copy of the row the same
+      }
+      // 32 channels at a time through shared memory (the Q tile's, which no
+      // product reads any more): copies of a row are added, and a row's
+      // channels leave side by side
+      float4 *stage = reinterpret_cast<float4 *>(smem + (kPair ? s * kOutTile : s * (kOutTile / 2)));
+      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * p.rows * kPartialStride;
+      constexpr int kChannels = kPair ? kHeadDim : kHeadDim / 2;
+      for (int c0 = 0; c0 < kChannels; c0 += 32) {
+        const int ch = (kPair ? 0 : s * kChannels) + c0;
+        float o[32];
+        if constexpr (kPair) {
+          tmem_ld32(tm_o + ch, o);
+          tmem_wait_ld32(o);
+        } else {
+          tmem_ld32(tmem + lanes + 256 + ch, o);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f0;
+          if (both) {
+            float o1[32];
+            tmem_ld32(tmem + lanes + 384 + ch, o1);
+            tmem_wait_ld32(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          stage[t * 8 + (c ^ (t & 7))] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        named_barrier(2 + s, kGroup);
+        for (int item = t; item < kRowsHere * 8; item += kGroup) {
+          const int r = item >> 3, c = item & 7, q_row = block + r, i = q_row >> p.group_log2;
+          if (i >= g.size) continue;
+          float4 v = stage[r * 8 + (c ^ (r & 7))];
+#pragma unroll
+          for (int k = 1; k < kRep; ++k) {
+            const float4 u = stage[(r + k * kRowsHere) * 8 + (c ^ (r & 7))];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+          }
+          const int channel = ch + 4 * c;
+          if (any_odd) {
+            const uint64_t in_tree = g.size >= 64 ? ~0ull : (1ull << g.size) - 1ull;
+            uint64_t bits = (p.mask != nullptr ? p.mask[static_cast<size_t>(g.b) * p.nodes + i] : (2ull << i) - 1ull) & in_tree;
+            float *y = &v.x;
+            for (; bits != 0; bits &= bits - 1) {
+              const size_t at = (static_cast<size_t>(bh) * p.capacity + first + __ffsll(static_cast<long long>(bits)) - 1) * kHeadDim + channel;
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (kByte) {
+                  if ((p.v[at + e] & 0x7Fu) == 0x7Fu) y[e] = __uint_as_float(0x7FFFFFFFu);
+                } else {
+                  const uint32_t x = reinterpret_cast<const uint16_t *>(p.v)[at + e];
+                  if ((x & 0x7F80u) == 0x7F80u) y[e] += bf16_f(x);
+                }
+              }
+            }
+          }
+          const float2 ml = row_s[s * kGroup + r];
+          if (whole) {
+            const float inv = 1.0f / ml.y;
+            float *y = &v.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = ml.y == 0.0f && y[e] == 0.0f ? 0.0f : y[e] * inv;
+            uint16_t *dst = p.out + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+                            (q_row & ((1 << p.group_log2) - 1)) * kHeadDim + channel;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          } else {
+            float *dst = part_out + static_cast<size_t>((kPair ? s * kGroup : 0) + r) * kPartialStride;
+            *reinterpret_cast<float4 *>(dst + channel) = v;
+            if (channel == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = ml;
+          }
+        }
+        named_barrier(2 + s, kGroup);
+      }
+      if (tid == 0 && g.tile0 == 0) {
+        // where merge_kernel finds the unit's parts: CTA c holds tiles
+        // floor(c total / ctas) on
+        const int64_t total = start_s[3], ctas = min(static_cast<int>(gridDim.x), start_s[3]);
+        const int64_t begin = static_cast<int64_t>(blockIdx.x) * total / ctas;
+        const int64_t done = static_cast<int64_t>(start_s[2]) - walk.left - g.tiles;  // before this segment
+        const int64_t last = begin + done + g.all - 1;
+        const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
+        p.table[static_cast<size_t>(g.b) * p.kv_heads * p.units_a_head + g.unit] =
+            make_int2(2 * static_cast<int>(blockIdx.x) + (starts ? 0 : 1), c1 - static_cast<int>(blockIdx.x) + 1);
+      }
+      starts = false;
+      tc_fence_before();
+      named_barrier(1, 2 * kGroup);
+      if (tid == 0) *odd = 0;
     }
   }
-  const float y = l == 0.0f ? 0.0f : o / l;
-  out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// --------------------------------------------------------------- the merge --
+
+// One CTA a row (sequence, node, head): joins the parts of a unit that several
+// CTAs shared, clears the rows of a bad sequence, and has nothing to do
+// otherwise.  Four warps take the parts in turn, four channels a lane.
+__global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
+  __shared__ float4 acc_s[4][32];
+  __shared__ float l_s[4];
+  const int heads = p.kv_heads << p.group_log2;
+  const int head = blockIdx.x % heads, bi = blockIdx.x / heads;
+  const int b = bi / p.nodes, i = bi - b * p.nodes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t *out = p.out + static_cast<size_t>(blockIdx.x) * kHeadDim;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Sequence q(p, b);
+  if (!q.good) {
+    if (threadIdx.x == 0 && i == 0 && head == 0) atomicOr(p.err, kFlagBadLength);
+    out[threadIdx.x] = 0;
+    return;
+  }
+  if (i >= q.size) return;
+  const int row = (i << p.group_log2) + (head & ((1 << p.group_log2) - 1));
+  const int kv = head >> p.group_log2, block = row / kTreeRows;
+  const int2 at = p.table[(static_cast<size_t>(b) * p.kv_heads + kv) * p.units_a_head + block];
+  // (a part count beyond the grid can only be left over from a call that gave up)
+  if (at.y <= 1 || at.x < 0 || (at.x >> 1) + at.y > p.ctas) return;
+  const float *base = p.partials + static_cast<size_t>(row - block * kTreeRows) * kPartialStride;
+  const size_t cta = static_cast<size_t>(2) * p.rows * kPartialStride;
+  // part 0 is in the slot that the table names, the others begin their CTAs: slot 0
+  const float *part0 = base + static_cast<size_t>(at.x) * p.rows * kPartialStride;
+  const float *parts = base + static_cast<size_t>(at.x >> 1) * cta;
+  float m = -INFINITY;
+  for (int k = lane; k < at.y; k += 32) m = fmaxf(m, (k == 0 ? part0 : parts + k * cta)[kHeadDim]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
+#pragma unroll 4
+  for (int k = warp; k < at.y; k += 4) {
+    const float *from = k == 0 ? part0 : parts + k * cta;
+    const float2 ml = *reinterpret_cast<const float2 *>(from + kHeadDim);
+    const float4 o = reinterpret_cast<const float4 *>(from)[lane];
+    const float f = exp2_f(ml.x - ref);
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+    l = fmaf(ml.y, f, l);
+  }
+  acc_s[warp][lane] = acc;
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  const float *a = reinterpret_cast<const float *>(acc_s) + threadIdx.x;
+  const float y = (a[0] + a[kHeadDim]) + (a[2 * kHeadDim] + a[3 * kHeadDim]);
+  const float total = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+  const float r = total == 0.0f && y == 0.0f ? 0.0f : y / total;
+  out[threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
+}
+
+// ----------------------------------------------------------------- launches --
+
+bool make_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, bool byte) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  if (byte) {
+    const cuuint64_t dims[2] = {kByteRow, rows}, strides[1] = {kByteRow};
+    const cuuint32_t box[2] = {kByteRow, kTile}, steps[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  // a row's two 128-byte halves as the outermost dimension: [half][token][64 channels] in shared memory
+  const cuuint64_t dims[3] = {64, rows, 2}, strides[2] = {2 * kHeadDim, 128};
+  const cuuint32_t box[3] = {64, kTile, 2}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kByte, int kCols, bool kPair>
+cudaError_t launch_as(const TreeParams &p, cudaStream_t stream) {
+  using L = Layout<kByte, kPair>;
+  static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(tree_kernel<kByte, kCols, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  CUtensorMap map_k, map_v;
+  const uint64_t rows = static_cast<uint64_t>(p.batch) * p.kv_heads * p.capacity;
+  if (!make_tensor_map(&map_k, p.k, rows, kByte) || !make_tensor_map(&map_v, p.v, rows, kByte))
+    return cudaErrorInvalidValue;
+  tree_kernel<kByte, kCols, kPair><<<p.ctas, kCtaThreads, L::kTotal, stream>>>(map_k, map_v, p);
+  return cudaGetLastError();
+}
+
+template <bool kByte>
+cudaError_t launch_format(const TreeParams &p, cudaStream_t stream) {
+  const int rows = p.nodes << p.group_log2;
+  if (rows <= 32) return launch_as<kByte, 32, false>(p, stream);
+  if (rows <= 64) return launch_as<kByte, 64, false>(p, stream);
+  if (rows <= 128) return launch_as<kByte, 128, false>(p, stream);
+  return launch_as<kByte, 128, true>(p, stream);
 }
 
 }  // namespace
 
-TreeLayout tree_layout(int32_t, int32_t, int32_t, int32_t) { return TreeLayout{256, 256}; }
+TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t nodes, int32_t capacity) {
+  TreeLayout L{};
+  const int rows = group * nodes;
+  L.units_a_head = (rows + kTreeRows - 1) / kTreeRows;
+  L.rows = rows < kTreeRows ? rows : kTreeRows;
+  const int64_t units = static_cast<int64_t>(batch) * kv_heads * L.units_a_head;
+  const int64_t tiles = units * ((static_cast<int64_t>(capacity) + kTile - 1) / kTile);
+  L.ctas = static_cast<int32_t>(tiles < kTreeCtas ? tiles : kTreeCtas);
+  L.table = 256;
+  L.partials = L.table + (static_cast<size_t>(units) * 8 + 255) / 256 * 256;
+  L.total = (L.partials + static_cast<size_t>(L.ctas) * 2 * L.rows * kPartialStride * 4 + 255) / 256 * 256;
+  return L;
+}
 
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.nodes), static_cast<unsigned>(p.kv_heads * p.group),
-                  static_cast<unsigned>(p.batch));
-  if (p.format == FFD_CACHE_BYTE)
-    tree_kernel<true><<<grid, kTile, 0, stream>>>(p);
-  else
-    tree_kernel<false><<<grid, kTile, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (p.ctas > 0) {
+    const cudaError_t e = p.format == FFD_CACHE_BYTE ? launch_format<true>(p, stream) : launch_format<false>(p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  // (starts while the kernel before it ends, and waits for it on the GPU)
+  cudaLaunchAttribute attribute{};
+  attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attribute.val.programmaticStreamSerializationAllowed = p.ctas > 0 ? 1 : 0;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(p.batch) * static_cast<unsigned>(p.nodes) *
+                        static_cast<unsigned>(p.kv_heads << p.group_log2));
+  config.blockDim = dim3(128);
+  config.stream = stream;
+  config.attrs = &attribute;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, merge_tree_kernel, p);
 }
 
 }  // namespace ffd
