@@ -105,6 +105,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
   }
 }
 
+// The same in five instructions, bounded by a count of attempts (each may rest
+// up to a microsecond): for warps that share an instruction cache with long
+// unrolled code and wait often.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 4194304;\n"
+      "again:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t@p bra over;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.u32 p, n, 0;\n\t@p bra again;\n"
+      "over:\n\tmov.u32 %0, n;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // ------------------------------------------------------------ bulk copies --
 
 // 1-D bulk copy global -> shared, completion counted on `bar` (bytes).
@@ -236,6 +252,18 @@ __device__ __forceinline__ uint32_t gather_mask_word(int w, int nb, int S, LoadW
 // Named barrier over `count` threads (multiple of 32).
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// The same, and whether `yes` holds in any of its threads.
+__device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t count, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"(yes ? 1u : 0u)
+      : "memory");
+  return any != 0;
 }
 
 }  // namespace ffd

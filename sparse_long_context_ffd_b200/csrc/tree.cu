@@ -24,99 +24,17 @@
 // multiplies the score in fp32; the V row's scale multiplies the weight, which
 // is the sum of two e4m3 parts too: 8 significant bits, in units of 2^-16 of
 // the largest weight so far, or finer.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <atomic>
 
-#include "ffd_ptx.cuh"
-#include "ffd_serve.h"
-#include "ffd_tcgen05.cuh"
+#include "ffd_tree.cuh"
 
 namespace ffd {
 namespace {
 
-constexpr int kTile = kTreeTile;
 constexpr int kGroup = 128;                  // threads of a softmax group
 constexpr int kCtaThreads = 3 * kGroup;       // and four warps, of which one copies and one multiplies
 constexpr int kSmemMax = 232448;
 constexpr int kOutTile = 32768;               // bytes of a Q tile (bf16, or two e4m3 parts)
-constexpr float kScoreScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
-
-__device__ __forceinline__ float bf16_f(uint32_t b) { return __uint_as_float(b << 16); }
-
-__device__ __forceinline__ float exp2_f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Two fp16 values as e4m3 `hi` and, of what is left, e4m3 `lo`.
-__device__ __forceinline__ void split_e4m3(uint32_t pair, uint32_t &hi, uint32_t &lo) {
-  uint16_t h, l;
-  uint32_t back, rest;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(pair));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
-  rest = sub_f16x2(pair, back);
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
-  hi = h;
-  lo = l;
-}
-
-// ------------------------------------------------------------------- work --
-
-struct Sequence {
-  int len, size;
-  bool good;
-  __device__ __forceinline__ Sequence(const TreeParams &p, int b) {
-    len = p.lengths[b];
-    size = p.sizes != nullptr ? p.sizes[b] : p.nodes;
-    good = len >= 0 && len <= p.capacity && size >= 0 && size <= p.nodes && size <= len;
-  }
-  // tiles of each of its units
-  __device__ __forceinline__ int tiles() const { return good && size > 0 ? (len + kTile - 1) / kTile : 0; }
-};
-
-struct Segment {
-  int b, unit, tile0, tiles, all;  // tiles of the unit in this CTA, and in all
-  int len, size;
-};
-
-// A CTA's part of the tile list, segment by segment.
-struct Walk {
-  int b, off, left;
-  __device__ __forceinline__ bool next(const TreeParams &p, Segment &g) {
-    if (left == 0) return false;
-    const int units = p.kv_heads * p.units_a_head;
-    for (; b < p.batch; ++b, off = 0) {
-      const Sequence q(p, b);
-      const int each = q.tiles();
-      if (off >= each * units) continue;
-      g.b = b;
-      g.unit = off / each;
-      g.tile0 = off - g.unit * each;
-      g.all = each;
-      g.tiles = min(each - g.tile0, left);
-      g.len = q.len;
-      g.size = q.size;
-      off += g.tiles;
-      left -= g.tiles;
-      return true;
-    }
-    return false;
-  }
-};
 
 // ------------------------------------------------------------------ layout --
 
@@ -129,7 +47,8 @@ struct Layout {
   static constexpr int kScales = kRing + kSlots * kSlot;               // [slot][K, V][128] bf16
   static constexpr int kTokens = kScales + (kByte ? kSlots * 512 : 0);  // [group][2][3][128] fp32
   static constexpr int kRow = kTokens + (kByte ? 2 * 2 * 3 * 512 : 0);  // [2][128] float2
-  static constexpr int kBars = kRow + 2 * kGroup * 8;
+  static constexpr int kScale = kRow + 2 * kGroup * 8;                  // [2][128] fp32, of the query rows
+  static constexpr int kBars = kScale + (kByte ? 2 * kGroup * 4 : 0);
   static constexpr int kNumBars = 2 * kSlots + 8;
   static constexpr int kWords = kBars + kNumBars * 8;
   static constexpr int kTotal = kWords + 32;
@@ -146,18 +65,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
   constexpr int kRep = kTile / kCols;        // copies of a row
   constexpr int kRowsHere = kGroup / kRep;   // rows of an accumulator
   constexpr int kSlots = L::kSlots;
-  constexpr uint32_t kIdescS = instr_desc(kByte ? 0 : 1, false), kIdescO = instr_desc(kByte ? 0 : 1, true);
+  constexpr uint32_t kIdescS = instr_desc(kByte ? 0 : 1, 128, false, false);
+  constexpr uint32_t kIdescO = instr_desc(kByte ? 0 : 1, 128, false, true);
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5;
   float2 *row_s = reinterpret_cast<float2 *>(smem + L::kRow);
+  float *scale_s = reinterpret_cast<float *>(smem + L::kScale);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
   uint64_t *full = bars, *empty = bars + kSlots;
-  uint64_t *bar_s = bars + 2 * kSlots, *bar_p = bar_s + 2, *bar_o = bar_s + 4, *bar_q = bar_s + 6;
+  uint64_t *bar_s = empty + kSlots, *bar_p = bar_s + 2, *bar_o = bar_s + 4, *bar_q = bar_s + 6;
   uint64_t *bar_end = bar_s + 7;
   volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
   volatile int *dead = words + 1;      // a wait ran out
   volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
-  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles
+  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
@@ -177,64 +98,27 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
-  {  // this CTA's part of the tiles: thread t adds up the sequences of its chunk
-    int *sum_s = reinterpret_cast<int *>(row_s);
-    const int chunk = (p.batch + kCtaThreads - 1) / kCtaThreads;
-    const int b0 = min(p.batch, tid * chunk), b1 = min(p.batch, b0 + chunk);
-    const int units = p.kv_heads * p.units_a_head;
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += Sequence(p, b).tiles() * units;
-    int upto = sum;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int other = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if ((tid & 31) >= d) upto += other;
-    }
-    if ((tid & 31) == 31) sum_s[warp] = upto;
-    __syncthreads();
-    int total = 0, before = upto - sum;
-    for (int w = 0; w < kCtaThreads / 32; ++w) {
-      if (w < warp) before += sum_s[w];
-      total += sum_s[w];
-    }
-    const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
-    int begin = 0, end = 0;
-    if (static_cast<int>(blockIdx.x) < ctas) {
-      begin = static_cast<int>(static_cast<int64_t>(blockIdx.x) * total / ctas);
-      end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / ctas);
-    }
-    if (begin >= before && begin < before + sum && end > begin) {
-      int off = begin - before, b = b0;
-      for (; b < b1; ++b) {
-        const int n = Sequence(p, b).tiles() * units;
-        if (off < n) break;
-        off -= n;
-      }
-      start_s[0] = b;
-      start_s[1] = off;
-      start_s[2] = end - begin;
-    }
-    if (tid == 0) start_s[3] = total;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-  }
+  find_part<kCtaThreads>(p, reinterpret_cast<int *>(row_s), start_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(words[0]);
   Walk walk{start_s[0], start_s[1], start_s[2]};
   Segment g;
 
-  // sticky: after one wait ran out nobody waits, loads or multiplies any more
-  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1;; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (*dead) return false;
-      if ((i & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
-        *dead = 1;
-        atomicOr(p.err, kFlagTimeout);
-        return false;
-      }
+  // A warp's answer to its lanes' waits: the same in every lane, which stand
+  // together again (they leave a wait one by one, and elect_one and the
+  // instructions under it are for a converged warp).
+  auto all = [](bool b) { return __all_sync(0xFFFFFFFFu, b) != 0; };
+  // After one wait ran out nobody waits, loads or multiplies any more.
+  bool alive = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (alive && !mbar_wait_short(bar, parity)) {
+      alive = false;
+      *dead = 1;
+      atomicOr(p.err, kFlagTimeout);
     }
+    return alive;
   };
 
   // Registers move from the last four warps to the softmax groups: 2 x 128 x
@@ -243,32 +127,32 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
     // ------------------------------------------------------------- copies --
-    if ((tid & 31) == 0) {
+    // (the whole warp walks and waits, one lane issues)
+    {
       uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
-      bool alive = true;
       while (alive && walk.next(p, g)) {
         const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
         for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
           const uint32_t slot = i % kSlots, round = i / kSlots;
-          if (round > 0 && !wait(empty + slot, (round - 1) & 1)) {
-            alive = false;
-            break;
-          }
+          if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1));
+          if (!alive) break;
           const int t0 = (g.tile0 + (j >> 1)) * kTile;
           const int row = bh * p.capacity + t0;
+          uint64_t *landed = full + slot;
           uint8_t *dst = smem + L::kRing + slot * L::kSlot;
           const void *map = (j & 1) ? &tmap_v : &tmap_k;
+          if (!elect_one()) continue;
           if constexpr (kByte) {
             const uint32_t scale_bytes = 2u * static_cast<uint32_t>(min(kTile, p.capacity - t0));
-            mbar_arrive_expect_tx(full + slot, L::kSlot + ((j & 1) ? 2 * scale_bytes : 0));
-            tma_load_2d(dst, map, 0, row, full + slot);
+            mbar_arrive_expect_tx(landed, L::kSlot + ((j & 1) ? 2 * scale_bytes : 0));
+            tma_load_2d(dst, map, 0, row, landed);
             if (j & 1) {
-              bulk_g2s(smem + L::kScales + slot * 512, p.k_scales + row, scale_bytes, full + slot);
-              bulk_g2s(smem + L::kScales + slot * 512 + 256, p.v_scales + row, scale_bytes, full + slot);
+              bulk_g2s(smem + L::kScales + slot * 512, p.k_scales + row, scale_bytes, landed);
+              bulk_g2s(smem + L::kScales + slot * 512 + 256, p.v_scales + row, scale_bytes, landed);
             }
           } else {
-            mbar_arrive_expect_tx(full + slot, L::kSlot);
-            tma_load_3d(dst, map, 0, row, 0, full + slot);
+            mbar_arrive_expect_tx(landed, L::kSlot);
+            tma_load_3d(dst, map, 0, row, 0, landed);
           }
         }
       }
@@ -278,67 +162,75 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ matrices --
-    if ((tid & 31) == 0) {
-      uint32_t n = 0, segments = 0, p_count[2] = {0, 0};
-      const uint32_t smem0 = smem_addr(smem);
-      bool alive = true;
-      auto scores = [&](int s, int j) {
-        const uint32_t i = 2 * (n + j), slot = i % kSlots;
-        alive = alive && wait(full + slot, (i / kSlots) & 1);
-        if (!alive) return;
-        tc_fence_after();
-        const uint32_t q = smem0 + (kPair ? s * kOutTile : 0), k = smem0 + L::kRing + slot * L::kSlot;
-        const uint32_t d = tmem + 128 * s;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          // bf16: 16 channels a step, four steps a 128-byte half; e4m3: 32
-          // channels a step, the row's first part and then its second
-          const uint32_t a = q + (c >> 2) * 16384 + (c & 3) * 32;
-          const uint32_t b = k + (kByte ? 0 : (c >> 2) * 16384) + (c & 3) * 32;
-          mma_ss<kByte>(d, smem_desc(a), smem_desc(b), kIdescS, c > 0);
+    // Item i of a segment is a tile's product pair for group i % 2.  S goes out
+    // when its K is there and the group's O += of the item before, over whose
+    // weights it is written, has gone out (products of a thread run in the order
+    // of their issue), O += when V and the weights are there, whichever is first.
+    // A commit holds the thread until what the last one stands for is done, and
+    // until the next issue the tensor cores stand still: so one commit a product
+    // where it can be, and lanes that ask the barriers at once.
+    uint32_t n = 0, segments = 0, p_phases = 0;
+    // (lane 0's copy: known to be the same in every lane, such values stay in
+    // uniform registers)
+    auto uniform = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    const uint32_t q0 = uniform(smem_addr(smem)), ring = q0 + L::kRing, tm0 = uniform(tmem);
+    const int lane = tid & 31;
+    while (alive && walk.next(p, g)) {
+      const int items = kPair ? 2 * g.tiles : g.tiles;
+      alive = all(wait(bar_q, segments & 1));
+      ++segments;
+      int si = 0, oi = 0;  // items whose S, whose O have gone out
+      uint32_t spin = 0;
+#pragma unroll 1
+      while (alive && oi < items) {
+        const uint32_t sg = uniform(si & 1), og = uniform(oi & 1);
+        const uint32_t ka = 2 * (n + (kPair ? si >> 1 : si)), va = 2 * (n + (kPair ? oi >> 1 : oi)) + 1;
+        const uint32_t k_slot = uniform(ka % kSlots), v_slot = uniform(va % kSlots);
+        uint64_t *bar = (lane & 1) ? full + v_slot : (lane & 2) ? bar_p + og : full + k_slot;
+        const uint32_t parity = (lane & 1) ? va / kSlots : (lane & 2) ? p_phases >> og : ka / kSlots;
+        const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity & 1));
+        const bool do_o = (yes & 6u) == 6u && oi < si;
+        const bool do_s = (yes & 1u) != 0 && si < items && si < oi + (do_o ? 3 : 2);
+        if (!do_s && !do_o) {
+          if (++spin < (1u << 23)) continue;
+          alive = false;
+          *dead = 1;
+          if (lane == 0) atomicOr(p.err, kFlagTimeout);
+          break;
         }
-        mma_commit(bar_s + s);
-        if (!kPair || s == 1) mma_commit(empty + slot);
-      };
-      auto values = [&](int s, int j, bool first) {
-        const uint32_t i = 2 * (n + j) + 1, slot = i % kSlots;
-        alive = alive && wait(bar_p + s, p_count[s] & 1) && wait(full + slot, (i / kSlots) & 1);
-        ++p_count[s];
-        if (!alive) return;
+        spin = 0;
         tc_fence_after();
-        const uint32_t a = tmem + 128 * s, v = smem0 + L::kRing + slot * L::kSlot, d = tmem + 256 + 128 * s;
+        if (do_o) {
+          const uint32_t add = uniform(oi < 2 ? 0 : 1), v = ring + v_slot * L::kSlot, tm = tm0 + 128 * og;
+          if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          // bf16: 16 tokens a step; e4m3: 32 tokens, first parts, then second
-          const uint32_t b = v + (kByte ? (c & 3) * 4096 : c * 2048);
-          mma_ts<kByte>(d, a + 8 * c, smem_desc(b, 16384), kIdescO, !first || c > 0);
-        }
-        if (!kPair || s == 1) mma_commit(empty + slot);
-      };
-      while (alive && walk.next(p, g)) {
-        alive = wait(bar_q, segments & 1);
-        ++segments;
-        for (int j = 0; alive && j <= g.tiles; ++j) {
-          if constexpr (kPair) {
-            for (int s = 0; s < 2; ++s) {
-              if (j > 0) values(s, j - 1, j == 1);
-              if (j < g.tiles) scores(s, j);
-              else if (alive) mma_commit(bar_o + s);
-            }
-          } else {
-            if (j < g.tiles) scores(j & 1, j);
-            if (j > 0) {
-              values((j - 1) & 1, j - 1, j <= 2);
-              if (alive && j - 1 >= g.tiles - 2) mma_commit(bar_o + ((j - 1) & 1));
-            }
+            for (int c = 0; c < 8; ++c)  // bf16: 16 tokens a step; e4m3: 32, first parts, then second
+              mma_ts<kByte>(tm + 256, tm + 8 * c, smem_desc(v + (kByte ? (c & 3) * 4096 : c * 2048), 16384), kIdescO,
+                            c > 0 || add != 0);
+            if (!kPair || og == 1) mma_commit(empty + v_slot);
+            if (oi >= items - 2) mma_commit(bar_o + og);
           }
+          p_phases ^= 1u << og;
+          ++oi;
         }
-        n += g.tiles;
+        if (do_s) {
+          const uint32_t k = ring + k_slot * L::kSlot, q = q0 + (kPair ? sg * kOutTile : 0), tm = tm0 + 128 * sg;
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)  // bf16: 16 channels a step, four a 128-byte half; e4m3: 32, Q's first part, then its second
+              mma_ss<kByte>(tm, smem_desc(q + (c >> 2) * 16384 + (c & 3) * 32),
+                            smem_desc(k + (kByte ? 0 : (c >> 2) * 16384) + (c & 3) * 32), kIdescS, c > 0);
+            mma_commit(bar_s + sg);
+          }
+          ++si;
+        }
+        __syncwarp();
       }
-      if (*dead) {  // what was issued is done before tensor memory is given back
-        mma_commit(bar_end);
-        mbar_wait(bar_end, 0, kWaitLimitNs);
-      }
+      n += g.tiles;
+    }
+    if (*dead) {  // what was issued is done before tensor memory is given back
+      if (elect_one()) mma_commit(bar_end);
+      mbar_wait(bar_end, 0, kWaitLimitNs);
     }
     }
   } else {
@@ -358,57 +250,64 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       const int block = (g.unit - head * p.units_a_head) * kTreeRows + (kPair ? s * kGroup : 0);
       const int first = g.len - g.size;
       const int bh = g.b * p.kv_heads + head;
-      // ---- the query rows ----
-      const int qr = block + row, node = qr >> p.group_log2;
-      const bool live = node < g.size;
+      // ---- the query rows: 16 threads a row, all loads before the first use ----
+      const uint64_t seen = seen_nodes(p, g, (block + row) >> p.group_log2);
       float score_scale = kScoreScale;
-      uint64_t seen = 0;
       {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (((static_cast<size_t>(g.b) * p.nodes + (live ? node : 0)) * p.kv_heads + head) << p.group_log2) * kHeadDim +
-            (qr & ((1 << p.group_log2) - 1)) * kHeadDim);
-        const uint64_t in_tree = g.size >= 64 ? ~0ull : (1ull << g.size) - 1ull;
-        if (live)
-          seen = (p.mask != nullptr ? p.mask[static_cast<size_t>(g.b) * p.nodes + node] : (2ull << node) - 1ull) & in_tree;
-        uint8_t *dst = smem + (kPair ? s * kOutTile : 0) + t * 128;
-        if constexpr (kByte) {
-          uint4 q[16];
-          uint32_t top = 0;
+        constexpr int kChunks = kRowsHere * 16 / (kPair ? kGroup : 2 * kGroup);
+        const int at = kPair ? t : tid, c = at & 15, r0 = at >> 4;
+        constexpr int kStep = (kPair ? kGroup : 2 * kGroup) / 16;
+        uint4 q[kChunks];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            q[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+        for (int k = 0; k < kChunks; ++k) {
+          const int qr = block + r0 + k * kStep, i = qr >> p.group_log2;
+          q[k] = make_uint4(0, 0, 0, 0);
+          if (i < g.size)
+            q[k] = __ldg(reinterpret_cast<const uint4 *>(
+                             p.q + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+                             (qr & ((1 << p.group_log2) - 1)) * kHeadDim) + c);
+        }
+        uint8_t *tile = smem + (kPair ? s * kOutTile : 0);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const int r = r0 + k * kStep;
+          if constexpr (kByte) {
+            const uint32_t x[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+            uint32_t top = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
-          }
-          // largest magnitude into [128, 256): in e4m3's range with all its bits
-          const int exponent = min(100, top == 0 ? 0 : 7 - ilogbf(bf16_f(top)));
-          const float up = top < 0x7F80u ? ldexpf(1.0f, exponent) : 0.0f;
-          score_scale = top < 0x7F80u ? ldexpf(kScoreScale, -exponent) : __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t hi[4], lo[4];
+            for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            // the largest magnitude into [128, 256) (a subnormal one, whose
+            // exponent reads as 0, below), by a power of two within fp32's range
+            const int exponent = top == 0 ? 0 : min(100, 134 - static_cast<int>(top >> 7));
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 &y = q[2 * c + (e >> 1)];
-              const uint32_t a = (e & 1) ? y.z : y.x, b = (e & 1) ? y.w : y.y;
-              uint32_t h0, l0, h1, l1;
-              split_e4m3(pack_f16(bf16_f(a & 0xFFFFu) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
-              split_e4m3(pack_f16(bf16_f(b & 0xFFFFu) * up, __uint_as_float(b & 0xFFFF0000u) * up), h1, l1);
-              hi[e] = h0 | h1 << 16;
-              lo[e] = l0 | l1 << 16;
+            for (int e = 0; e < 2; ++e)
+              split4_signed(bf16_f(x[2 * e] & 0xFFFFu) * up, __uint_as_float(x[2 * e] & 0xFFFF0000u) * up,
+                            bf16_f(x[2 * e + 1] & 0xFFFFu) * up, __uint_as_float(x[2 * e + 1] & 0xFFFF0000u) * up, hi[e], lo[e]);
+#pragma unroll
+            for (int copy = 0; copy < kRep; ++copy) {
+              const int rr = r + copy * kRowsHere;
+              uint8_t *dst = tile + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
+              *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2 *>(dst + 16384) = make_uint2(lo[0], lo[1]);
             }
-            const int at = (c ^ (t & 7)) << 4;
-            if (kPair || s == 0) *reinterpret_cast<uint4 *>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (kPair || s == 1) *reinterpret_cast<uint4 *>(dst + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
+            if (c == 0)
+              scale_s[(kPair ? s * kGroup : 0) + r] = top < 0x7F80u ? kScoreScale * down : __uint_as_float(0x7FFFFFFFu);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (!kPair && (c >> 3) != s) continue;
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4)) =
-                live ? src[c] : make_uint4(0, 0, 0, 0);
+            for (int copy = 0; copy < kRep; ++copy) {
+              const int rr = r + copy * kRowsHere;
+              *reinterpret_cast<uint4 *>(tile + rr * 128 + (c >> 3) * 16384 + (((c & 7) ^ (rr & 7)) << 4)) = q[k];
+            }
           }
+        }
+        if constexpr (kByte) {
+          if constexpr (kPair) named_barrier(2 + s, kGroup); else named_barrier(1, 2 * kGroup);
+          score_scale = scale_s[(kPair ? s * kGroup : 0) + row];
         }
       }
       fence_proxy_async_smem();
@@ -423,10 +322,19 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         const uint32_t vi = 2 * (n + j) + 1, v_slot = vi % kSlots;
         const float4 *tok = nullptr;  // [3][kCols]: K scale, V scale, its log2
         if constexpr (kByte) {
-          wait(full + v_slot, (vi / kSlots) & 1);
+          wait(full + vi % kSlots, (vi / kSlots) & 1);
           const uint16_t *raw = reinterpret_cast<const uint16_t *>(smem + L::kScales + v_slot * 512);
           float *mine = reinterpret_cast<float *>(smem + L::kTokens) + (s * 2 + (s_count & 1)) * 3 * kTile;
-          const float vs = bf16_f(raw[kTile + t]);
+          float vs = bf16_f(raw[kTile + t]);
+          if (masked && t0 + t >= first) {
+            // (a weight of zero must not meet a scale that is not finite: as for values, below)
+            if (t0 + t >= g.len) {
+              vs = 0.0f;
+            } else if (!(fabsf(vs) < INFINITY)) {
+              vs = 0.0f;
+              *odd = 1;
+            }
+          }
           mine[t] = bf16_f(raw[t]);
           mine[kTile + t] = vs;
           // (a zero scale: far below any other, but not infinitely far)
@@ -438,12 +346,13 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         wait(bar_s + s, s_count & 1);
         ++s_count;
         tc_fence_after();
+        if ((kPair ? s == 1 : true) && t == 0) mbar_arrive(empty + (vi - 1) % kSlots);  // K is read
         float x[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld32(tm_s + part * kCols + c, x + c);
-        tmem_wait_ld32(x);
+        for (int c = 0; c < kCols; c += 32) tmem_ld<32>(tm_s + part * kCols + c, x + c);
+        tmem_wait_ld<32>(x);
 #pragma unroll
-        for (int c = 32; c < kCols; c += 32) tmem_tie32(x + c);
+        for (int c = 32; c < kCols; c += 32) tmem_wait_ld<32, false>(x + c);
         if constexpr (kByte) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
@@ -501,8 +410,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
           for (int c = 0; c < kHeadDim; c += 32) {
             float o[32];
-            tmem_ld32(tm_o + c, o);
-            tmem_wait_ld32(o);
+            tmem_ld<32>(tm_o + c, o);
+            tmem_wait_ld<32>(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= f;
             tmem_st<32>(tm_o + c, reinterpret_cast<const uint32_t *>(o));
@@ -521,16 +430,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             sum[1] += p1;
             sum[2] += p2;
             sum[3] += p3;
-            // (an unseen token's scale may be anything)
-            const float w0 = masked && x[c] == -INFINITY ? 0.0f : p0 * vs.x;
-            const float w1 = masked && x[c + 1] == -INFINITY ? 0.0f : p1 * vs.y;
-            const float w2 = masked && x[c + 2] == -INFINITY ? 0.0f : p2 * vs.z;
-            const float w3 = masked && x[c + 3] == -INFINITY ? 0.0f : p3 * vs.w;
-            uint32_t h0, l0, h1, l1;
-            split_e4m3(pack_f16(w0, w1), h0, l0);
-            split_e4m3(pack_f16(w2, w3), h1, l1);
-            hi[c >> 2] = h0 | h1 << 16;
-            lo[c >> 2] = l0 | l1 << 16;
+            split4(p0 * vs.x, p1 * vs.y, p2 * vs.z, p3 * vs.w, hi[c >> 2], lo[c >> 2]);
           }
           constexpr int kWide = kCols / 4;
           uint32_t none[kWide];
@@ -573,48 +473,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         if (masked) {
-          // A weight of zero must not meet a value that is not finite.  Rows
-          // past the sequence hold anything; a drafted token's row may hold
-          // infinities or NaN that some nodes see: they are taken out here and
-          // put back, for those nodes, at the end.
           wait(full + v_slot, (vi / kSlots) & 1);
-          const int token = t0 + t;
-          if (token >= first) {
-            uint4 *v = reinterpret_cast<uint4 *>(smem + L::kRing + v_slot * L::kSlot + t * 128);
-            bool bad = false;
-            for (int c = 0; c < (kByte ? 8 : 16); ++c) {
-              uint4 &y = v[(c >> 3) * 1024 + ((c + t) & 7)];
-              if (token >= g.len) {
-                y = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint32_t x4[4] = {y.x, y.y, y.z, y.w};
-              bool changed = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (kByte) {
-#pragma unroll
-                  for (int h = 0; h < 32; h += 8)
-                    if (((x4[e] >> h) & 0x7Fu) == 0x7Fu) {
-                      x4[e] &= ~(0xFFu << h);
-                      changed = true;
-                    }
-                } else {
-#pragma unroll
-                  for (int h = 0; h < 32; h += 16)
-                    if (((x4[e] >> h) & 0x7F80u) == 0x7F80u) {
-                      x4[e] &= ~(0xFFFFu << h);
-                      changed = true;
-                    }
-                }
-              }
-              if (changed) {
-                y = make_uint4(x4[0], x4[1], x4[2], x4[3]);
-                bad = true;
-              }
-            }
-            if (bad) *odd = 1;
-          }
+          if (t0 + t >= first &&
+              clean_values<kByte>(smem + L::kRing + v_slot * L::kSlot, t, t0 + t >= g.len, 0, kByte ? 8 : 16))
+            *odd = 1;
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -661,17 +523,17 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         const int ch = (kPair ? 0 : s * kChannels) + c0;
         float o[32];
         if constexpr (kPair) {
-          tmem_ld32(tm_o + ch, o);
-          tmem_wait_ld32(o);
+          tmem_ld<32>(tm_o + ch, o);
+          tmem_wait_ld<32>(o);
         } else {
-          tmem_ld32(tmem + lanes + 256 + ch, o);
-          tmem_wait_ld32(o);
+          tmem_ld<32>(tmem + lanes + 256 + ch, o);
+          tmem_wait_ld<32>(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= f0;
           if (both) {
             float o1[32];
-            tmem_ld32(tmem + lanes + 384 + ch, o1);
-            tmem_wait_ld32(o1);
+            tmem_ld<32>(tmem + lanes + 384 + ch, o1);
+            tmem_wait_ld<32>(o1);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
           }
@@ -694,20 +556,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
           }
           const int channel = ch + 4 * c;
           if (any_odd) {
-            const uint64_t in_tree = g.size >= 64 ? ~0ull : (1ull << g.size) - 1ull;
-            uint64_t bits = (p.mask != nullptr ? p.mask[static_cast<size_t>(g.b) * p.nodes + i] : (2ull << i) - 1ull) & in_tree;
+            const uint64_t bits = seen_nodes(p, g, i);
             float *y = &v.x;
-            for (; bits != 0; bits &= bits - 1) {
-              const size_t at = (static_cast<size_t>(bh) * p.capacity + first + __ffsll(static_cast<long long>(bits)) - 1) * kHeadDim + channel;
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (kByte) {
-                  if ((p.v[at + e] & 0x7Fu) == 0x7Fu) y[e] = __uint_as_float(0x7FFFFFFFu);
-                } else {
-                  const uint32_t x = reinterpret_cast<const uint16_t *>(p.v)[at + e];
-                  if ((x & 0x7F80u) == 0x7F80u) y[e] += bf16_f(x);
-                }
-              }
-            }
+            for (int e = 0; e < 4; ++e) y[e] += odd_values<kByte>(p, g, bh, bits, channel + e);
           }
           const float2 ml = row_s[s * kGroup + r];
           if (whole) {
@@ -726,17 +577,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         }
         named_barrier(2 + s, kGroup);
       }
-      if (tid == 0 && g.tile0 == 0) {
-        // where merge_kernel finds the unit's parts: CTA c holds tiles
-        // floor(c total / ctas) on
-        const int64_t total = start_s[3], ctas = min(static_cast<int>(gridDim.x), start_s[3]);
-        const int64_t begin = static_cast<int64_t>(blockIdx.x) * total / ctas;
-        const int64_t done = static_cast<int64_t>(start_s[2]) - walk.left - g.tiles;  // before this segment
-        const int64_t last = begin + done + g.all - 1;
-        const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
-        p.table[static_cast<size_t>(g.b) * p.kv_heads * p.units_a_head + g.unit] =
-            make_int2(2 * static_cast<int>(blockIdx.x) + (starts ? 0 : 1), c1 - static_cast<int>(blockIdx.x) + 1);
-      }
+      if (tid == 0 && g.tile0 == 0) note_unit(p, g, walk, start_s, starts);
       starts = false;
       tc_fence_before();
       named_barrier(1, 2 * kGroup);
@@ -759,7 +600,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 // otherwise.  Four warps take the parts in turn, four channels a lane.
 __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   __shared__ float4 acc_s[4][32];
-  __shared__ float l_s[4];
+  __shared__ float2 ml_s[4];
   const int heads = p.kv_heads << p.group_log2;
   const int head = blockIdx.x % heads, bi = blockIdx.x / heads;
   const int b = bi / p.nodes, i = bi - b * p.nodes;
@@ -783,31 +624,54 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   // part 0 is in the slot that the table names, the others begin their CTAs: slot 0
   const float *part0 = base + static_cast<size_t>(at.x) * p.rows * kPartialStride;
   const float *parts = base + static_cast<size_t>(at.x >> 1) * cta;
-  float m = -INFINITY;
-  for (int k = lane; k < at.y; k += 32) m = fmaxf(m, (k == 0 ? part0 : parts + k * cta)[kHeadDim]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  const float ref = m == -INFINITY ? 0.0f : m;
+  // four parts' loads in flight a warp, joined on a running maximum
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f;
-#pragma unroll 4
-  for (int k = warp; k < at.y; k += 4) {
-    const float *from = k == 0 ? part0 : parts + k * cta;
-    const float2 ml = *reinterpret_cast<const float2 *>(from + kHeadDim);
-    const float4 o = reinterpret_cast<const float4 *>(from)[lane];
-    const float f = exp2_f(ml.x - ref);
-    acc.x = fmaf(o.x, f, acc.x);
-    acc.y = fmaf(o.y, f, acc.y);
-    acc.z = fmaf(o.z, f, acc.z);
-    acc.w = fmaf(o.w, f, acc.w);
-    l = fmaf(ml.y, f, l);
+  float l = 0.0f, m = -INFINITY;
+  for (int k0 = warp; k0 < at.y; k0 += 16) {
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + 4 * u;
+      ml[u] = make_float2(-INFINITY, 0.0f);
+      o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k < at.y) {
+        const float *from = k == 0 ? part0 : parts + k * cta;
+        ml[u] = *reinterpret_cast<const float2 *>(from + kHeadDim);
+        o[u] = reinterpret_cast<const float4 *>(from)[lane];
+      }
+    }
+    const float next = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+    const float ref = next == -INFINITY ? 0.0f : next, fade = exp2_f(m - ref);
+    m = next;
+    acc.x *= fade;
+    acc.y *= fade;
+    acc.z *= fade;
+    acc.w *= fade;
+    l *= fade;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = exp2_f(ml[u].x - ref);
+      acc.x = fmaf(o[u].x, f, acc.x);
+      acc.y = fmaf(o[u].y, f, acc.y);
+      acc.z = fmaf(o[u].z, f, acc.z);
+      acc.w = fmaf(o[u].w, f, acc.w);
+      l = fmaf(ml[u].y, f, l);
+    }
   }
   acc_s[warp][lane] = acc;
-  if (lane == 0) l_s[warp] = l;
+  if (lane == 0) ml_s[warp] = make_float2(m, l);
   __syncthreads();
-  const float *a = reinterpret_cast<const float *>(acc_s) + threadIdx.x;
-  const float y = (a[0] + a[kHeadDim]) + (a[2 * kHeadDim] + a[3 * kHeadDim]);
-  const float total = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+  float top = -INFINITY, y = 0.0f, total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, ml_s[w].x);
+  if (top == -INFINITY) top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = exp2_f(ml_s[w].x - top);
+    y = fmaf(reinterpret_cast<const float *>(acc_s[w])[threadIdx.x], f, y);
+    total = fmaf(ml_s[w].y, f, total);
+  }
   const float r = total == 0.0f && y == 0.0f ? 0.0f : y / total;
   out[threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
 }
@@ -833,7 +697,7 @@ bool make_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, bool byt
 }
 
 template <bool kByte, int kCols, bool kPair>
-cudaError_t launch_as(const TreeParams &p, cudaStream_t stream) {
+cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
   using L = Layout<kByte, kPair>;
   static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised
   int dev = 0;
@@ -845,21 +709,25 @@ cudaError_t launch_as(const TreeParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  CUtensorMap map_k, map_v;
-  const uint64_t rows = static_cast<uint64_t>(p.batch) * p.kv_heads * p.capacity;
-  if (!make_tensor_map(&map_k, p.k, rows, kByte) || !make_tensor_map(&map_v, p.v, rows, kByte))
-    return cudaErrorInvalidValue;
   tree_kernel<kByte, kCols, kPair><<<p.ctas, kCtaThreads, L::kTotal, stream>>>(map_k, map_v, p);
   return cudaGetLastError();
 }
 
-template <bool kByte>
-cudaError_t launch_format(const TreeParams &p, cudaStream_t stream) {
+cudaError_t launch_rows_of(const TreeParams &p, cudaStream_t stream) {
+  const bool byte = p.format == FFD_CACHE_BYTE;
+  CUtensorMap map_k, map_v;
+  const uint64_t tokens = static_cast<uint64_t>(p.batch) * p.kv_heads * p.capacity;
+  if (!make_tensor_map(&map_k, p.k, tokens, byte) || !make_tensor_map(&map_v, p.v, tokens, byte))
+    return cudaErrorInvalidValue;
   const int rows = p.nodes << p.group_log2;
-  if (rows <= 32) return launch_as<kByte, 32, false>(p, stream);
-  if (rows <= 64) return launch_as<kByte, 64, false>(p, stream);
-  if (rows <= 128) return launch_as<kByte, 128, false>(p, stream);
-  return launch_as<kByte, 128, true>(p, stream);
+  if (rows <= 16) return launch_tree_narrow(p, map_k, map_v, stream);
+  if (rows <= 32)
+    return byte ? launch_as<true, 32, false>(p, map_k, map_v, stream) : launch_as<false, 32, false>(p, map_k, map_v, stream);
+  if (rows <= 64)
+    return byte ? launch_as<true, 64, false>(p, map_k, map_v, stream) : launch_as<false, 64, false>(p, map_k, map_v, stream);
+  if (rows <= 128)
+    return byte ? launch_as<true, 128, false>(p, map_k, map_v, stream) : launch_as<false, 128, false>(p, map_k, map_v, stream);
+  return byte ? launch_as<true, 128, true>(p, map_k, map_v, stream) : launch_as<false, 128, true>(p, map_k, map_v, stream);
 }
 
 }  // namespace
@@ -880,7 +748,7 @@ TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t n
 
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream) {
   if (p.ctas > 0) {
-    const cudaError_t e = p.format == FFD_CACHE_BYTE ? launch_format<true>(p, stream) : launch_format<false>(p, stream);
+    const cudaError_t e = launch_rows_of(p, stream);
     if (e != cudaSuccess) return e;
   }
   // (starts while the kernel before it ends, and waits for it on the GPU)

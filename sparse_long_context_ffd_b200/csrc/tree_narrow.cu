@@ -1,0 +1,606 @@
+// tree_narrow.cu -- drafted-token attention with up to 64 query rows a kv-head.
+//
+// Tokens are the 128 lanes of an accumulator and query rows its columns, S^T =
+// K Q^T and O^T += V^T P^T: a matrix instruction's time goes with its columns,
+// so few rows cost little (with rows as lanes 128 of them are paid for), and a
+// thread has one token, whose scale and visibility it keeps in registers.  The
+// weights' reference m of a row is the same for all tokens; whether any score
+// passes it is one vote a tile, and only then are maxima taken over the lanes.
+//
+// e4m3: the two parts of a query row are two columns' worth of S^T, added in
+// fp32, and those of a weight two columns of O^T, added at the end: K and V
+// pass through the tensor cores once.
+//
+// Groups of 128 threads take the tiles in turn, with an S and an O each.
+#include <atomic>
+
+#include "ffd_tree.cuh"
+
+namespace ffd {
+namespace {
+
+constexpr int kSmemMax = 232448;
+// second parts of query rows are kept times 2^4, those of weights times 2^3
+constexpr int kQLo = 4, kWLo = 3;
+constexpr float kNever = -3.0e38f;  // the reference of a row that has seen nothing
+
+template <bool kByte, int kRows>
+struct Narrow {
+  // More groups hide more of a tile's latency.  A K that waits for its turn
+  // behind kGroups V's must find a slot: 2 kGroups of them at least.
+  static constexpr int kGroups = kByte && kRows == 16 ? 4 : 2;
+  static constexpr int kParts = kRows == 16 ? 1 : 2;        // threads of a token, each with its rows
+  static constexpr int kT = kRows / kParts;                 // rows of a thread
+  static constexpr int kGroup = kParts * 128;               // threads of a group
+  static constexpr int kThreads = kGroups * kGroup + 128;   // the last four warps copy and multiply
+  static constexpr int kN = kByte ? 2 * kRows : kRows;      // columns of S and O
+  static constexpr int kRowBytes = kByte ? kN : 2 * kN;     // of a token's weights
+  static constexpr int kTmem = 2 * kGroups * kN <= 128 ? 128 : 2 * kGroups * kN <= 256 ? 256 : 512;
+  static constexpr int kSlot = kByte ? 16384 : 32768;       // bytes of K or V of a tile
+  static constexpr int kQ = kByte ? kN * 128 : kN * 256;
+  static constexpr int kWeights = kQ;                       // [group][128 tokens][kRowBytes]
+  static constexpr int kRing = kWeights + kGroups * 128 * kRowBytes;
+  static constexpr int kSlots = kByte ? 10 : kRows == 64 ? 4 : 6;
+  static constexpr int kScales = kRing + kSlots * kSlot;    // [slot][128] bf16
+  static constexpr int kRef = kScales + (kByte ? kSlots * 256 : 0);  // [group][kRows] m
+  static constexpr int kFade = kRef + kGroups * kRows * 4;  // [group][kRows]
+  static constexpr int kWarpRow = kFade + kGroups * kRows * 4;  // [group][4 warps][kRows]
+  static constexpr int kSeen = kWarpRow + kGroups * 4 * kRows * 4;  // [kRows]
+  static constexpr int kTot = kSeen + kRows * 8;            // [kRows] (m, sum); largest query magnitudes
+  static constexpr int kBars = kTot + kRows * 8;
+  static constexpr int kNumBars = 2 * kSlots + 3 * kGroups + 2;
+  static constexpr int kWords = kBars + kNumBars * 8;
+  static constexpr int kTotal = kWords + 32;
+  static_assert(kTotal <= kSmemMax, "shared memory");
+  // (even: a slot then holds K's only or V's only, as `idle` below needs)
+  static_assert(kSlots >= 2 * kGroups && kSlots % 2 == 0, "the ring would stop");
+  static_assert(kRing % 1024 == 0 && 2 * kGroups * kN <= kTmem, "layout");
+};
+
+// For each of 16 rows the 32 lanes' v[row] joined (sum, or largest): lane t has
+// row t / 2, in v[0].
+template <bool kMax>
+__device__ __forceinline__ void join_lanes(float *v, int lane) {
+  auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1) {
+    const bool up = lane & (2 * n);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = join(keep, __shfl_xor_sync(0xFFFFFFFFu, send, 2 * n));
+    }
+  }
+  v[0] = join(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+}
+
+template <bool kByte, int kRows>
+__global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
+    tree_narrow_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const TreeParams p) {
+  using L = Narrow<kByte, kRows>;
+  constexpr int kGroups = L::kGroups, kN = L::kN, kSlots = L::kSlots, kRowBytes = L::kRowBytes;
+  constexpr int kGroup = L::kGroup, kT = L::kT;
+  constexpr int kSteps = kByte ? 4 : 8;  // matrix instructions of a product
+  constexpr uint32_t kIdescS = instr_desc(kByte ? 0 : 1, kN, false, false);
+  constexpr uint32_t kIdescO = instr_desc(kByte ? 0 : 1, kN, true, true);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
+  uint64_t *full = bars, *empty = bars + kSlots, *bar_s = empty + kSlots, *bar_p = bar_s + kGroups,
+           *bar_f = bar_p + kGroups, *bar_q = bar_f + kGroups, *bar_end = bar_q + 1;
+  float *ref_s = reinterpret_cast<float *>(smem + L::kRef);
+  float *fade_s = reinterpret_cast<float *>(smem + L::kFade);
+  float *warp_row_s = reinterpret_cast<float *>(smem + L::kWarpRow);
+  float2 *tot_s = reinterpret_cast<float2 *>(smem + L::kTot);
+  uint64_t *seen_s = reinterpret_cast<uint64_t *>(smem + L::kSeen);
+  volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
+  volatile int *dead = words + 1;      // a wait ran out
+  volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
+  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
+  constexpr int kMatrixWarp = kGroups * kGroup / 32, kCopyWarp = kMatrixWarp + 1;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == kMatrixWarp) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), L::kTmem);
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
+    for (int s = 0; s < kGroups; ++s) {
+      mbar_init(bar_s + s, 1);
+      mbar_init(bar_p + s, kGroup);
+      mbar_init(bar_f + s, 1);
+    }
+    mbar_init(bar_q, kGroups * kGroup);
+    mbar_init(bar_end, 1);
+    fence_mbar_init();
+    *dead = 0;
+    *odd = 0;
+    start_s[0] = start_s[1] = start_s[2] = 0;
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  find_part<L::kThreads>(p, reinterpret_cast<int *>(warp_row_s), start_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(words[0]);
+  Walk walk{start_s[0], start_s[1], start_s[2]};
+  Segment g;
+
+  // A warp's answer to its lanes' waits: the same in every lane, which stand
+  // together again (they leave a wait one by one, and elect_one and the
+  // instructions under it are for a converged warp).
+  auto all = [](bool b) { return __all_sync(0xFFFFFFFFu, b) != 0; };
+  // After one wait ran out nobody waits, loads or multiplies any more.
+  bool alive = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (alive && !mbar_wait_short(bar, parity)) {
+      alive = false;
+      *dead = 1;
+      atomicOr(p.err, kFlagTimeout);
+    }
+    return alive;
+  };
+
+  if (warp == kCopyWarp) {
+    // ------------------------------------------------------------- copies --
+    // (the whole warp walks and waits, one lane issues)
+    uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
+    while (alive && walk.next(p, g)) {
+      const int bh = g.b * p.kv_heads + g.unit;
+      for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
+        const uint32_t slot = i % kSlots, round = i / kSlots;
+        if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1));
+        if (!alive) break;
+        const int t0 = (g.tile0 + (j >> 1)) * kTile;
+        const int row = bh * p.capacity + t0;
+        uint64_t *landed = full + slot;
+        uint8_t *dst = smem + L::kRing + slot * L::kSlot;
+        const void *map = (j & 1) ? &tmap_v : &tmap_k;
+        if (!elect_one()) continue;
+        if constexpr (kByte) {
+          // (each copy brings its scales)
+          const uint32_t scale_bytes = 2u * static_cast<uint32_t>(min(kTile, p.capacity - t0));
+          mbar_arrive_expect_tx(landed, L::kSlot + scale_bytes);
+          tma_load_2d(dst, map, 0, row, landed);
+          bulk_g2s(smem + L::kScales + slot * 256, ((j & 1) ? p.v_scales : p.k_scales) + row, scale_bytes, landed);
+        } else {
+          mbar_arrive_expect_tx(landed, L::kSlot);
+          tma_load_3d(dst, map, 0, row, 0, landed);
+        }
+      }
+    }
+    __syncwarp();
+    if (*dead)  // what is in flight lands before the CTA ends
+      for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
+        mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
+  } else if (warp == kMatrixWarp) {
+    // ------------------------------------------------------------ matrices --
+    // Tile i of a segment is group i % kGroups'.  S of a tile goes out when its K
+    // is there and the group has read its last S, O += of one when V and the
+    // weights are there, whichever is first: neither holds up the other's slot.
+    // A commit holds the thread until what the last one stands for is done, and
+    // until the next issue the tensor cores stand still: so one commit a product,
+    // and four lanes ask the four barriers at once.
+    uint32_t n = 0, segments = 0, p_phases = 0, f_phases = (1u << kGroups) - 1u;
+    // (lane 0's copy: known to be the same in every lane, such values stay in
+    // uniform registers)
+    auto uniform = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    const uint32_t q = uniform(smem_addr(smem)), ring = q + L::kRing, tm = uniform(tmem);
+    while (alive && walk.next(p, g)) {
+      alive = all(wait(bar_q, segments & 1));
+      ++segments;
+      int si = 0, oi = 0;  // tiles whose S, whose O have gone out
+      uint32_t spin = 0;
+#pragma unroll 1
+      while (alive && oi < g.tiles) {
+        const uint32_t sg = uniform(si % kGroups), og = uniform(oi % kGroups);
+        const uint32_t ka = 2 * (n + si), va = 2 * (n + oi) + 1;
+        const uint32_t k_slot = uniform(ka % kSlots), v_slot = uniform(va % kSlots);
+        uint64_t *bar = (lane & 2) ? ((lane & 1) ? bar_p + og : full + v_slot) : ((lane & 1) ? bar_f + sg : full + k_slot);
+        const uint32_t parity = (lane & 2) ? ((lane & 1) ? p_phases >> og : va / kSlots) : ((lane & 1) ? f_phases >> sg : ka / kSlots);
+        const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity & 1));
+        const bool do_s = (yes & 3u) == 3u && si < g.tiles, do_o = (yes & 12u) == 12u && oi < si;
+        if (!do_s && !do_o) {
+          if (++spin < (1u << 23)) continue;
+          alive = false;
+          *dead = 1;
+          if (lane == 0) atomicOr(p.err, kFlagTimeout);
+          break;
+        }
+        spin = 0;
+        tc_fence_after();
+        if (do_o) {
+          const uint32_t add = uniform(oi < kGroups ? 0 : 1), v = ring + v_slot * L::kSlot;
+          const uint32_t d = tm + (kGroups + og) * kN, w = q + L::kWeights + og * 128 * kRowBytes;
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)  // bf16: 16 tokens a step; e4m3: 32
+              mma_ss<kByte>(d, smem_desc(v + c * (kByte ? 4096 : 2048), 16384),
+                            smem_desc<kRowBytes>(w + c * (kByte ? 32 : 16) * kRowBytes), kIdescO, c > 0 || add != 0);
+            mma_commit(empty + v_slot);
+          }
+          p_phases ^= 1u << og;
+          ++oi;
+        }
+        if (do_s) {
+          const uint32_t k = ring + k_slot * L::kSlot, d = tm + sg * kN;
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)  // bf16: 16 channels a step, four a 128-byte half; e4m3: 32
+              mma_ss<kByte>(d, smem_desc(k + (c >> 2) * 16384 + (c & 3) * 32),
+                            smem_desc(q + (c >> 2) * kN * 128 + (c & 3) * 32), kIdescS, c > 0);
+            mma_commit(bar_s + sg);
+          }
+          f_phases ^= 1u << sg;
+          ++si;
+        }
+        __syncwarp();
+      }
+      n += g.tiles;
+    }
+    if (*dead) {  // what was issued is done before tensor memory is given back
+      if (elect_one()) mma_commit(bar_end);
+      mbar_wait(bar_end, 0, kWaitLimitNs);
+    }
+  } else if (warp < kMatrixWarp) {
+    // ------------------------------------------------------------- softmax --
+    const int team = warp >> 2, s = team / L::kParts, w = warp & 3;  // group; which 32 lanes of an accumulator
+    const int rb = team % L::kParts * kT;        // this thread's rows, from rb on
+    const int t = tid & 127;                     // token of a tile; channel of O
+    const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
+    const uint32_t tm_s = tmem + lanes + s * kN, tm_o = tmem + lanes + (kGroups + s) * kN;
+    const uint32_t bar_group = 1 + s, bar_all = 5;
+    float *ref = ref_s + s * kRows;
+    float *fade = fade_s + s * kRows;
+    // The weights of a group are read and its O is idle when V's slot is empty
+    // again.  (The slot's next V belongs to a later tile, whose product comes
+    // after the one that this group has still to ask for.)
+    auto idle = [&](uint32_t v) { return wait(empty + v % kSlots, (v / kSlots) & 1); };
+    uint32_t last_v = 0;                         // copy of V of the group's last tile
+    uint32_t count = 0, n = 0;                   // tiles of this group so far; of the CTA
+    bool starts = true;                          // the CTA's first segment
+    while (walk.next(p, g)) {
+      const int head = g.unit;
+      const int first = g.len - g.size;
+      const int bh = g.b * p.kv_heads + head;
+      // ---- the query rows: 16 threads a row, all loads before the first use ----
+      // e4m3: all rows are scaled by one power of two, the largest magnitude into
+      // [128, 256).  (What a small row loses is below what a large one's scores
+      // are off by; a softmax goes by differences.)
+      float score_scale = kScoreScale;
+      {
+        constexpr int kAll = kGroups * kGroup, kChunks = (kRows * 16 + kAll - 1) / kAll, kStep = kAll / 16;
+        const int c = tid & 15, r0 = tid >> 4;
+        uint4 x[kChunks];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const int r = r0 + k * kStep, i = r >> p.group_log2;
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (r < kRows && i < g.size)
+            x[k] = __ldg(reinterpret_cast<const uint4 *>(
+                             p.q + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+                             (r & ((1 << p.group_log2) - 1)) * kHeadDim) + c);
+        }
+        if (tid < kRows) seen_s[tid] = seen_nodes(p, g, tid >> p.group_log2);
+        if (tid < kGroups * kRows) ref_s[tid] = kNever;
+        uint32_t tops[kChunks], most = 0;
+        if constexpr (kByte) {
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            tops[k] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tops[k] = max(tops[k], max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) tops[k] = max(tops[k], __shfl_xor_sync(0xFFFFFFFFu, tops[k], d));
+            if (tops[k] < 0x7F80u) most = max(most, tops[k]);
+          }
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+          uint32_t *most_s = reinterpret_cast<uint32_t *>(tot_s);
+          if (lane == 0) most_s[warp] = most;
+          named_barrier(bar_all, kAll);
+          most = 0;
+#pragma unroll
+          for (int i = 0; i < kAll / 32; ++i) most = max(most, most_s[i]);
+        }
+        const int exponent = most == 0 ? 0 : min(100, 134 - static_cast<int>(most >> 7));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
+        if constexpr (kByte) score_scale *= __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const int r = r0 + k * kStep;
+          if (r >= kRows) continue;
+          if constexpr (kByte) {
+            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            const float by = tops[k] < 0x7F80u ? up : __uint_as_float(0x7FFFFFFFu);  // (an infinity spoils its row)
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              split4_signed<kQLo>(bf16_f(v[2 * e] & 0xFFFFu) * by, __uint_as_float(v[2 * e] & 0xFFFF0000u) * by,
+                                  bf16_f(v[2 * e + 1] & 0xFFFFu) * by, __uint_as_float(v[2 * e + 1] & 0xFFFF0000u) * by, hi[e], lo[e]);
+            // first parts are rows 0 on, second parts kRows on
+            uint8_t *dst = smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(dst + kRows * 128) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint4 *>(smem + r * 128 + (c >> 3) * kRows * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[k];
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar_q);
+      named_barrier(bar_all, kGroups * kGroup);
+
+      // ---- the tiles ----
+      float l[kT];
+#pragma unroll
+      for (int r = 0; r < kT; ++r) l[r] = 0.0f;
+      uint32_t here = 0;                         // of this segment's
+      for (int j = s; j < g.tiles; j += kGroups, ++here) {
+        const int t0 = (g.tile0 + j) * kTile, token = t0 + t;
+        const bool masked = t0 + kTile > first;
+        const uint32_t vi = 2 * (n + j) + 1, v_slot = vi % kSlots, k_slot = (vi - 1) % kSlots;
+        wait(bar_s + s, count & 1);
+        tc_fence_after();
+        float ks = score_scale, vs = 1.0f, lv = 0.0f;
+        if constexpr (kByte) {
+          ks *= bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + k_slot * 256)[t]);
+          wait(full + v_slot, (vi / kSlots) & 1);
+          vs = bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + v_slot * 256)[t]);
+          if (masked && token >= first) {
+            // (a weight of zero must not meet a scale that is not finite: as for values, below)
+            if (token >= g.len) {
+              vs = 0.0f;
+            } else if (!(fabsf(vs) < INFINITY)) {
+              vs = 0.0f;
+              *odd = 1;
+            }
+          }
+          lv = __log2f(fabsf(vs));
+          lv = lv < -60.0f ? -60.0f : lv;  // (a zero scale: far below any other, but not infinitely far)
+        }
+        // 16 rows' scores of the token, in units of log 2, above m of `below`
+        auto load = [&](int c, float *x, auto below) {
+          tmem_ld<16>(tm_s + c, x);
+          if constexpr (kByte) {
+            float x2[16];
+            tmem_ld<16>(tm_s + kRows + c, x2);
+            tmem_wait_ld<16>(x);
+            tmem_wait_ld<16, false>(x2);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(x2[e], 1.0f / (1 << kQLo), x[e]);
+          } else {
+            tmem_wait_ld<16>(x);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 m = below(c + e);
+            x[e] = fmaf(x[e], ks, -m.x);
+            x[e + 1] = fmaf(x[e + 1], ks, -m.y);
+            x[e + 2] = fmaf(x[e + 2], ks, -m.z);
+            x[e + 3] = fmaf(x[e + 3], ks, -m.w);
+          }
+          if (masked && token >= first) {
+            const int at = token - first;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (at >= 64 || !((seen_s[c + e] >> (at & 63)) & 1ull)) x[e] = -INFINITY;
+          }
+        };
+        auto above_m = [&](int r) { return *reinterpret_cast<const float4 *>(ref + r); };
+        // The reference m of a row moves only when weights would leave their
+        // range: in bf16 past 2^8; in e4m3 past 448 (2^8.8), from 2^4 at the last
+        // move, so that small weights keep their bits.
+        constexpr float kRoom = kByte ? 8.8f : 8.0f, kAbove = kByte ? 4.0f : 0.0f;
+        float z[kT], top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kT; c += 16) {
+          load(rb + c, z + c, above_m);
+#pragma unroll
+          for (int r = c; r < c + 16; ++r) top = fmaxf(top, z[r]);
+        }
+        if (here > 0) idle(last_v);
+        last_v = vi;
+        tc_fence_before();
+        const bool move = named_barrier_any(bar_group, kGroup, top > kRoom - lv);
+        const bool speaks = (tid & (kGroup - 1)) == 0;
+        if (speaks) mbar_arrive(empty + k_slot);  // K and its scales are read
+        if (move) {
+#pragma unroll 1
+          for (int c = rb; c < rb + kT; c += 16) {
+            float v[16];
+            load(c, v, [&](int) { return make_float4(-lv, -lv, -lv, -lv); });
+            join_lanes<true>(v, lane);
+            if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + c + (lane >> 1)] = v[0];
+          }
+          named_barrier(bar_group, kGroup);
+          const int r = tid & (kGroup - 1);
+          if (r < kRows) {
+            const float *of = warp_row_s + 4 * s * kRows + r;
+            const float high = fmaxf(fmaxf(of[0], of[kRows]), fmaxf(of[2 * kRows], of[3 * kRows]));
+            const float m = ref[r], next = high > m + kRoom ? high - kAbove : m;
+            ref[r] = next;
+            fade[r] = next == m ? 1.0f : exp2_f(m - next);
+          }
+          named_barrier(bar_group, kGroup);
+#pragma unroll
+          for (int c = 0; c < kT; c += 16) load(rb + c, z + c, above_m);
+#pragma unroll
+          for (int e = 0; e < kT; ++e) l[e] *= fade[rb + e];
+          if (here > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kN / L::kParts; c += 16) {
+              const int at = c + team % L::kParts * (kN / L::kParts);
+              float o[16];
+              tmem_ld<16>(tm_o + at, o);
+              tmem_wait_ld<16>(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= fade[(at & (kRows - 1)) + e];
+              tmem_st<16>(tm_o + at, reinterpret_cast<const uint32_t *>(o));
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          named_barrier(bar_group, kGroup);
+        }
+        if (speaks) mbar_arrive(bar_f + s);  // S is read
+        // ---- weights ----
+        uint8_t *mine = smem + L::kWeights + (s * 128 + t) * kRowBytes;
+        // 16-byte vector c of a token's row under the swizzle of its span
+        auto swizzle = [&](int c) {
+          return (kRowBytes == 128 ? c ^ (t & 7) : kRowBytes == 64 ? c ^ ((t >> 1) & 3) : c ^ ((t >> 2) & 1)) << 4;
+        };
+#pragma unroll
+        for (int r = 0; r < kT; r += kByte ? 16 : 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < (kByte ? 16 : 8); e += 4) {
+            const float p0 = exp2_f(z[r + e]), p1 = exp2_f(z[r + e + 1]);
+            const float p2 = exp2_f(z[r + e + 2]), p3 = exp2_f(z[r + e + 3]);
+            l[r + e] += p0;
+            l[r + e + 1] += p1;
+            l[r + e + 2] += p2;
+            l[r + e + 3] += p3;
+            if constexpr (kByte) {
+              split4<kWLo>(p0 * vs, p1 * vs, p2 * vs, p3 * vs, hi[e >> 2], lo[e >> 2]);
+            } else {
+              hi[e >> 1] = pack_bf16(p0, p1);
+              hi[(e >> 1) + 1] = pack_bf16(p2, p3);
+            }
+          }
+          if constexpr (kByte) {
+            *reinterpret_cast<uint4 *>(mine + swizzle((rb + r) >> 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(mine + swizzle((kRows + rb + r) >> 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint4 *>(mine + swizzle((rb + r) >> 3)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          }
+        }
+        if (masked) {
+          constexpr int kVectors = (kByte ? 8 : 16) / L::kParts;
+          wait(full + v_slot, (vi / kSlots) & 1);
+          if (token >= first &&
+              clean_values<kByte>(smem + L::kRing + v_slot * L::kSlot, t, token >= g.len,
+                                  team % L::kParts * kVectors, (team % L::kParts + 1) * kVectors))
+            *odd = 1;
+        }
+        ++count;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar_p + s);
+      }
+      n += g.tiles;
+
+      // ---- the end of a segment: the groups' sums and O together ----
+      if (here > 0) idle(last_v);
+#pragma unroll
+      for (int c = 0; c < kT; c += 16) {
+        join_lanes<false>(l + c, lane);
+        if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + rb + c + (lane >> 1)] = l[c];
+      }
+      tc_fence_after();
+      named_barrier(bar_all, kGroups * kGroup);
+      const bool whole = g.tiles == g.all;
+      const bool any_odd = *odd != 0;
+      const int used = min(g.tiles, kGroups);  // groups that have an O
+      if (tid < kRows) {  // a row's reference and sum, and what its O's are multiplied with
+        float m = kNever, sum = 0.0f;
+        for (int u = 0; u < used; ++u) m = fmaxf(m, ref_s[u * kRows + tid]);
+        for (int u = 0; u < used; ++u) {
+          const float *of = warp_row_s + 4 * u * kRows + tid;
+          const float f = exp2_f(ref_s[u * kRows + tid] - m);
+          fade_s[u * kRows + tid] = f;
+          sum += ((of[0] + of[kRows]) + (of[2 * kRows] + of[3 * kRows])) * f;
+        }
+        tot_s[tid] = make_float2(m, sum);
+        warp_row_s[tid] = 1.0f / sum;
+      }
+      named_barrier(bar_all, kGroups * kGroup);
+      // four rows at a time, 32 channels a warp, one a lane
+      constexpr int kMine = kRows / (kGroups * L::kParts);
+      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * p.rows * kPartialStride;
+#pragma unroll 1
+      for (int r0 = team * kMine; r0 < (team + 1) * kMine && (r0 >> p.group_log2) < g.size; r0 += 4) {
+        float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int u = 0; u < used; ++u) {
+          float v[4], v2[4];
+          tmem_ld<4>(tmem + lanes + (kGroups + u) * kN + r0, v);
+          if constexpr (kByte) tmem_ld<4>(tmem + lanes + (kGroups + u) * kN + kRows + r0, v2);
+          tmem_wait_ld<4>(v);
+          if constexpr (kByte) {
+            tmem_wait_ld<4, false>(v2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(v2[e], 1.0f / (1 << kWLo), v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], fade_s[u * kRows + r0 + e], o[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + e, i = r >> p.group_log2;
+          if (i < g.size) {
+            if (any_odd) o[e] += odd_values<kByte>(p, g, bh, seen_s[r], t);
+            if (whole) {
+              const float y = tot_s[r].y == 0.0f && o[e] == 0.0f ? 0.0f : o[e] * warp_row_s[r];
+              p.out[((((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) +
+                     (r & ((1 << p.group_log2) - 1))) * kHeadDim + t] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+            } else {
+              float *dst = part_out + static_cast<size_t>(r) * kPartialStride;
+              dst[t] = o[e];
+              if (t == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = tot_s[r];
+            }
+          }
+        }
+      }
+      if (tid == 0 && g.tile0 == 0) note_unit(p, g, walk, start_s, starts);
+      starts = false;
+      tc_fence_before();
+      named_barrier(bar_all, kGroups * kGroup);
+      if (tid == 0) *odd = 0;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMatrixWarp) {
+    tc_fence_after();
+    tmem_free(tmem, L::kTmem);
+  }
+}
+
+template <bool kByte, int kRows>
+cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
+  using L = Narrow<kByte, kRows>;
+  static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(tree_narrow_kernel<kByte, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  tree_narrow_kernel<kByte, kRows><<<p.ctas, L::kThreads, L::kTotal, stream>>>(map_k, map_v, p);
+  return cudaGetLastError();
+}
+
+template <bool kByte>
+cudaError_t launch_format(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
+  const int rows = p.nodes << p.group_log2;
+  if (rows <= 16) return launch_as<kByte, 16>(p, map_k, map_v, stream);
+  if (rows <= 32) return launch_as<kByte, 32>(p, map_k, map_v, stream);
+  return launch_as<kByte, 64>(p, map_k, map_v, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_narrow(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                               cudaStream_t stream) {
+  return p.format == FFD_CACHE_BYTE ? launch_format<true>(p, map_k, map_v, stream)
+                                    : launch_format<false>(p, map_k, map_v, stream);
+}
+
+}  // namespace ffd

@@ -299,3 +299,37 @@ def test_long_cache(fmt):
             want, mag = (p @ vv).cpu(), (p @ vv.abs()).cpu()
             tol = want.abs() * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -10)
             assert ((got[b, :, h] - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n,G", [(1, 4), (7, 8), (16, 4), (13, 8), (64, 4), (63, 8)])
+def test_long_cache_row_tiles(fmt, n, G):
+    """Every tile of query rows over caches long enough that the copies, not
+    the products, set the pace; checked on the GPU in 64 bits."""
+    B, Hkv, cap = 2, 4, 65536
+    c = Case(fmt, B, n, G, Hkv, 256, [256, 256 - 77], seed=17)
+    s = su.shape(B, G, Hkv, cap)
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn((B, Hkv, cap, 128), generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    if fmt == ffd.FFD_CACHE_BYTE:
+        (kc, ks), (vc, vs) = su.quantise64(k.float()), su.quantise64(v.float())
+        cache = ffd.KVCache(kc, vc, ks, vs)
+        k, v = kc.double() * ks.double()[..., None], vc.double() * vs.double()[..., None]
+    else:
+        cache = ffd.KVCache(k, v)
+    lengths = [cap, cap - 12345]
+    q, out, ws = c.q.cuda(), torch.zeros_like(c.q).cuda(), ffd.tree_workspace(s, n)
+    mask = torch.tensor([su.signed(w) for w in c.words]).cuda()
+    ln = torch.tensor(lengths, dtype=torch.int32).cuda()
+    for _ in range(3):
+        ffd.decode_tree(s, cache, q, ln, out, ws, tree_mask=mask)
+    assert ffd.check_device_status(ws) == 0
+    for b, L in enumerate(lengths):
+        seen = torch.ones((n, L), dtype=torch.bool, device="cuda")
+        seen[:, L - n:] = (mask[b][:, None] >> torch.arange(n, device="cuda")) & 1 != 0
+        for h in range(G * Hkv):
+            kk, vv = k[b, h // G, :L].double(), v[b, h // G, :L].double()
+            p = torch.softmax((q[b, :, h].double() @ kk.T / 128 ** 0.5).masked_fill(~seen, -float("inf")), -1)
+            want, mag = p @ vv, p @ vv.abs()
+            tol = want.abs() * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -10)
+            assert ((out[b, :, h].double() - want).abs() <= tol).all()
