@@ -66,6 +66,6 @@ struct TreeLayout {
 TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t nodes, int32_t capacity);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
 cudaError_t launch_tree_narrow(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
-                               cudaStream_t stream);  // at most 64 rows; without the merge
+                               cudaStream_t stream);  // at most 16 rows; without the merge
 
 }  // namespace ffd

@@ -60,7 +60,7 @@ struct Layout {
 template <bool kByte, int kCols, bool kPair>
 __global__ void __launch_bounds__(kCtaThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                const TreeParams p) {
+                const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
   using L = Layout<kByte, kPair>;
   constexpr int kRep = kTile / kCols;        // copies of a row
   constexpr int kRowsHere = kGroup / kRep;   // rows of an accumulator
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       mbar_init(bar_p + s, kGroup);
       mbar_init(bar_o + s, 1);
     }
-    mbar_init(bar_q, 2 * kGroup);
+    mbar_init(bar_q, kByte ? 2 * kGroup : 1);
     mbar_init(bar_end, 1);
     fence_mbar_init();
     *dead = 0;
@@ -253,25 +253,24 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       // ---- the query rows: 16 threads a row, all loads before the first use ----
       const uint64_t seen = seen_nodes(p, g, (block + row) >> p.group_log2);
       float score_scale = kScoreScale;
-      {
-        constexpr int kChunks = kRowsHere * 16 / (kPair ? kGroup : 2 * kGroup);
+      if constexpr (kByte) {
+        constexpr int kThreads = kPair ? kGroup : 2 * kGroup, kStep = kThreads / 16, kChunks = kRowsHere / kStep;
         const int at = kPair ? t : tid, c = at & 15, r0 = at >> 4;
-        constexpr int kStep = (kPair ? kGroup : 2 * kGroup) / 16;
+        // (kStep is a multiple of the group: a chunk further is whole nodes on)
+        const int i0 = (block + r0) >> p.group_log2, step = kStep >> p.group_log2;
+        const size_t heads = static_cast<size_t>(p.kv_heads) << p.group_log2;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + ((static_cast<size_t>(g.b) * p.nodes + i0) * heads + (head << p.group_log2) +
+                   ((block + r0) & ((1 << p.group_log2) - 1))) * kHeadDim) + c;
         uint4 q[kChunks];
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int qr = block + r0 + k * kStep, i = qr >> p.group_log2;
-          q[k] = make_uint4(0, 0, 0, 0);
-          if (i < g.size)
-            q[k] = __ldg(reinterpret_cast<const uint4 *>(
-                             p.q + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
-                             (qr & ((1 << p.group_log2) - 1)) * kHeadDim) + c);
-        }
+        for (int k = 0; k < kChunks; ++k)
+          q[k] = i0 + k * step < g.size ? __ldg(src + k * step * heads * 16) : make_uint4(0, 0, 0, 0);
         uint8_t *tile = smem + (kPair ? s * kOutTile : 0);
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
           const int r = r0 + k * kStep;
-          if constexpr (kByte) {
+          {
             const uint32_t x[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
             uint32_t top = 0;
 #pragma unroll
@@ -297,22 +296,24 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             }
             if (c == 0)
               scale_s[(kPair ? s * kGroup : 0) + r] = top < 0x7F80u ? kScoreScale * down : __uint_as_float(0x7FFFFFFFu);
-          } else {
-#pragma unroll
-            for (int copy = 0; copy < kRep; ++copy) {
-              const int rr = r + copy * kRowsHere;
-              *reinterpret_cast<uint4 *>(tile + rr * 128 + (c >> 3) * 16384 + (((c & 7) ^ (rr & 7)) << 4)) = q[k];
-            }
           }
         }
-        if constexpr (kByte) {
-          if constexpr (kPair) named_barrier(2 + s, kGroup); else named_barrier(1, 2 * kGroup);
-          score_scale = scale_s[(kPair ? s * kGroup : 0) + row];
+        if constexpr (kPair) named_barrier(2 + s, kGroup); else named_barrier(1, 2 * kGroup);
+        score_scale = scale_s[(kPair ? s * kGroup : 0) + row];
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar_q);
+      } else if (tid == 0) {
+        // rows past the tree are whatever lies there: no other row's result has anything of them
+        constexpr int kTiles = kPair ? 2 : 1;
+        mbar_arrive_expect_tx(bar_q, kTiles * kOutTile);
+#pragma unroll
+        for (int i = 0; i < 2 * kTiles * kRep; ++i) {
+          const int q_tile = i / (2 * kRep), half = i & 1, copy = (i >> 1) % kRep;
+          tma_load_4d(smem + q_tile * kOutTile + half * 16384 + copy * kRowsHere * 128, &tmap_q, half * 64, 0, head,
+                      g.b * p.nodes + ((block + q_tile * kGroup) >> p.group_log2), bar_q);
         }
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(bar_q);
 
       // ---- the tiles ----
       float m = -INFINITY, l = 0.0f;
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       if (tid == 0 && g.tile0 == 0) note_unit(p, g, walk, start_s, starts);
       starts = false;
       tc_fence_before();
+      fence_proxy_async_smem();  // the next Q comes over what was staged
       named_barrier(1, 2 * kGroup);
       if (tid == 0) *odd = 0;
     }
@@ -696,8 +698,25 @@ bool make_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, bool byt
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [node][kv-head][head of the group][channel]: a box is `rows`
+// rows of one kv-head, half of the channels.
+bool make_query_map(CUtensorMap *map, const TreeParams &p, int rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint32_t group = 1u << p.group_log2;
+  const cuuint64_t dims[4] = {kHeadDim, group, static_cast<cuuint64_t>(p.kv_heads),
+                              static_cast<cuuint64_t>(p.batch) * p.nodes};
+  const cuuint64_t strides[3] = {2 * kHeadDim, 2 * kHeadDim * group, 2 * kHeadDim * group * dims[2]};
+  const cuuint32_t box[4] = {64, group, 1, static_cast<cuuint32_t>(rows) / group}, steps[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(p.q), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kByte, int kCols, bool kPair>
 cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
+  CUtensorMap map_q{};
+  if (!kByte && !make_query_map(&map_q, p, kCols)) return cudaErrorInvalidValue;  // (kCols rows, too: 128 / copies)
   using L = Layout<kByte, kPair>;
   static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised
   int dev = 0;
@@ -709,7 +728,7 @@ cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUten
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_kernel<kByte, kCols, kPair><<<p.ctas, kCtaThreads, L::kTotal, stream>>>(map_k, map_v, p);
+  tree_kernel<kByte, kCols, kPair><<<p.ctas, kCtaThreads, L::kTotal, stream>>>(map_k, map_v, map_q, p);
   return cudaGetLastError();
 }
 

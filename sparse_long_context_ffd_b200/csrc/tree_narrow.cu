@@ -1,4 +1,4 @@
-// tree_narrow.cu -- drafted-token attention with up to 64 query rows a kv-head.
+// tree_narrow.cu -- drafted-token attention with up to 16 query rows a kv-head.
 //
 // Tokens are the 128 lanes of an accumulator and query rows its columns, S^T =
 // K Q^T and O^T += V^T P^T: a matrix instruction's time goes with its columns,
@@ -19,28 +19,29 @@
 namespace ffd {
 namespace {
 
+constexpr int kGroup = 128;      // threads of a group
+constexpr int kRowBytes = 32;     // of a token's weights: 16 rows in bf16, or two e4m3 parts
 constexpr int kSmemMax = 232448;
 // second parts of query rows are kept times 2^4, those of weights times 2^3
 constexpr int kQLo = 4, kWLo = 3;
 constexpr float kNever = -3.0e38f;  // the reference of a row that has seen nothing
 
-template <bool kByte, int kRows>
+constexpr int kRows = 16;
+
+template <bool kByte>
 struct Narrow {
-  // More groups hide more of a tile's latency.  A K that waits for its turn
-  // behind kGroups V's must find a slot: 2 kGroups of them at least.
-  static constexpr int kGroups = kByte && kRows == 16 ? 4 : 2;
-  static constexpr int kParts = kRows == 16 ? 1 : 2;        // threads of a token, each with its rows
-  static constexpr int kT = kRows / kParts;                 // rows of a thread
-  static constexpr int kGroup = kParts * 128;               // threads of a group
-  static constexpr int kThreads = kGroups * kGroup + 128;   // the last four warps copy and multiply
+  // More groups hide more of a tile's latency, which a tile of bf16, twice as
+  // long in coming, hides with two.  A K that waits for its turn behind kGroups
+  // V's must find a slot: 2 kGroups of them at least.
+  static constexpr int kGroups = kByte ? 4 : 2;
+  static constexpr int kThreads = (kGroups + 1) * kGroup;   // the last four warps copy and multiply
   static constexpr int kN = kByte ? 2 * kRows : kRows;      // columns of S and O
-  static constexpr int kRowBytes = kByte ? kN : 2 * kN;     // of a token's weights
-  static constexpr int kTmem = 2 * kGroups * kN <= 128 ? 128 : 2 * kGroups * kN <= 256 ? 256 : 512;
+  static constexpr int kTmem = kByte ? 256 : 128;
   static constexpr int kSlot = kByte ? 16384 : 32768;       // bytes of K or V of a tile
-  static constexpr int kQ = kByte ? kN * 128 : kN * 256;
+  static constexpr int kQ = 4096;                           // the query rows
   static constexpr int kWeights = kQ;                       // [group][128 tokens][kRowBytes]
   static constexpr int kRing = kWeights + kGroups * 128 * kRowBytes;
-  static constexpr int kSlots = kByte ? 10 : kRows == 64 ? 4 : 6;
+  static constexpr int kSlots = kByte ? 10 : 6;
   static constexpr int kScales = kRing + kSlots * kSlot;    // [slot][128] bf16
   static constexpr int kRef = kScales + (kByte ? kSlots * 256 : 0);  // [group][kRows] m
   static constexpr int kFade = kRef + kGroups * kRows * 4;  // [group][kRows]
@@ -74,13 +75,12 @@ __device__ __forceinline__ void join_lanes(float *v, int lane) {
   v[0] = join(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-template <bool kByte, int kRows>
-__global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
+template <bool kByte>
+__global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     tree_narrow_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const TreeParams p) {
-  using L = Narrow<kByte, kRows>;
-  constexpr int kGroups = L::kGroups, kN = L::kN, kSlots = L::kSlots, kRowBytes = L::kRowBytes;
-  constexpr int kGroup = L::kGroup, kT = L::kT;
+  using L = Narrow<kByte>;
+  constexpr int kGroups = L::kGroups, kN = L::kN, kSlots = L::kSlots;
   constexpr int kSteps = kByte ? 4 : 8;  // matrix instructions of a product
   constexpr uint32_t kIdescS = instr_desc(kByte ? 0 : 1, kN, false, false);
   constexpr uint32_t kIdescO = instr_desc(kByte ? 0 : 1, kN, true, true);
@@ -244,8 +244,7 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
     }
   } else if (warp < kMatrixWarp) {
     // ------------------------------------------------------------- softmax --
-    const int team = warp >> 2, s = team / L::kParts, w = warp & 3;  // group; which 32 lanes of an accumulator
-    const int rb = team % L::kParts * kT;        // this thread's rows, from rb on
+    const int s = warp >> 2, w = warp & 3;       // group; which 32 lanes of an accumulator
     const int t = tid & 127;                     // token of a tile; channel of O
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t tm_s = tmem + lanes + s * kN, tm_o = tmem + lanes + (kGroups + s) * kN;
@@ -269,62 +268,44 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
       // are off by; a softmax goes by differences.)
       float score_scale = kScoreScale;
       {
-        constexpr int kAll = kGroups * kGroup, kChunks = (kRows * 16 + kAll - 1) / kAll, kStep = kAll / 16;
-        const int c = tid & 15, r0 = tid >> 4;
-        uint4 x[kChunks];
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int r = r0 + k * kStep, i = r >> p.group_log2;
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (r < kRows && i < g.size)
-            x[k] = __ldg(reinterpret_cast<const uint4 *>(
-                             p.q + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
-                             (r & ((1 << p.group_log2) - 1)) * kHeadDim) + c);
-        }
+        const int c = tid & 15, r = tid >> 4, i = r >> p.group_log2;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < kRows && i < g.size)
+          x = __ldg(reinterpret_cast<const uint4 *>(
+                        p.q + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+                        (r & ((1 << p.group_log2) - 1)) * kHeadDim) + c);
         if (tid < kRows) seen_s[tid] = seen_nodes(p, g, tid >> p.group_log2);
         if (tid < kGroups * kRows) ref_s[tid] = kNever;
-        uint32_t tops[kChunks], most = 0;
         if constexpr (kByte) {
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+          uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            tops[k] = 0;
+          for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tops[k] = max(tops[k], max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) tops[k] = max(tops[k], __shfl_xor_sync(0xFFFFFFFFu, tops[k], d));
-            if (tops[k] < 0x7F80u) most = max(most, tops[k]);
-          }
+          for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          uint32_t most = top < 0x7F80u ? top : 0;
           most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
           uint32_t *most_s = reinterpret_cast<uint32_t *>(tot_s);
           if (lane == 0) most_s[warp] = most;
-          named_barrier(bar_all, kAll);
+          named_barrier(bar_all, kGroups * kGroup);
           most = 0;
 #pragma unroll
-          for (int i = 0; i < kAll / 32; ++i) most = max(most, most_s[i]);
-        }
-        const int exponent = most == 0 ? 0 : min(100, 134 - static_cast<int>(most >> 7));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
-        if constexpr (kByte) score_scale *= __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+          for (int e = 0; e < kRows / 2; ++e) most = max(most, most_s[e]);
+          const int exponent = most == 0 ? 0 : min(100, 134 - static_cast<int>(most >> 7));
+          score_scale *= __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+          const float by = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 + exponent) << 23 : 0x7FFFFFFFu);  // (an infinity spoils its row)
+          uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int r = r0 + k * kStep;
-          if (r >= kRows) continue;
-          if constexpr (kByte) {
-            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            const float by = tops[k] < 0x7F80u ? up : __uint_as_float(0x7FFFFFFFu);  // (an infinity spoils its row)
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              split4_signed<kQLo>(bf16_f(v[2 * e] & 0xFFFFu) * by, __uint_as_float(v[2 * e] & 0xFFFF0000u) * by,
-                                  bf16_f(v[2 * e + 1] & 0xFFFFu) * by, __uint_as_float(v[2 * e + 1] & 0xFFFF0000u) * by, hi[e], lo[e]);
-            // first parts are rows 0 on, second parts kRows on
+          for (int e = 0; e < 2; ++e)
+            split4_signed<kQLo>(bf16_f(v[2 * e] & 0xFFFFu) * by, __uint_as_float(v[2 * e] & 0xFFFF0000u) * by,
+                                bf16_f(v[2 * e + 1] & 0xFFFFu) * by, __uint_as_float(v[2 * e + 1] & 0xFFFF0000u) * by, hi[e], lo[e]);
+          if (r < kRows) {  // first parts are rows 0 on, second parts kRows on
             uint8_t *dst = smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
             *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2 *>(dst + kRows * 128) = make_uint2(lo[0], lo[1]);
-          } else {
-            *reinterpret_cast<uint4 *>(smem + r * 128 + (c >> 3) * kRows * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[k];
           }
+        } else {
+          *reinterpret_cast<uint4 *>(smem + r * 128 + (c >> 3) * kRows * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
         }
       }
       fence_proxy_async_smem();
@@ -333,9 +314,9 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
       named_barrier(bar_all, kGroups * kGroup);
 
       // ---- the tiles ----
-      float l[kT];
+      float l[kRows];
 #pragma unroll
-      for (int r = 0; r < kT; ++r) l[r] = 0.0f;
+      for (int r = 0; r < kRows; ++r) l[r] = 0.0f;
       uint32_t here = 0;                         // of this segment's
       for (int j = s; j < g.tiles; j += kGroups, ++here) {
         const int t0 = (g.tile0 + j) * kTile, token = t0 + t;
@@ -360,12 +341,12 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
           lv = __log2f(fabsf(vs));
           lv = lv < -60.0f ? -60.0f : lv;  // (a zero scale: far below any other, but not infinitely far)
         }
-        // 16 rows' scores of the token, in units of log 2, above m of `below`
-        auto load = [&](int c, float *x, auto below) {
-          tmem_ld<16>(tm_s + c, x);
+        // the token's scores, in units of log 2, above m of `below`
+        auto load = [&](float *x, auto below) {
+          tmem_ld<16>(tm_s, x);
           if constexpr (kByte) {
             float x2[16];
-            tmem_ld<16>(tm_s + kRows + c, x2);
+            tmem_ld<16>(tm_s + kRows, x2);
             tmem_wait_ld<16>(x);
             tmem_wait_ld<16, false>(x2);
 #pragma unroll
@@ -375,7 +356,7 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 m = below(c + e);
+            const float4 m = below(e);
             x[e] = fmaf(x[e], ks, -m.x);
             x[e + 1] = fmaf(x[e + 1], ks, -m.y);
             x[e + 2] = fmaf(x[e + 2], ks, -m.z);
@@ -385,7 +366,7 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
             const int at = token - first;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (at >= 64 || !((seen_s[c + e] >> (at & 63)) & 1ull)) x[e] = -INFINITY;
+              if (at >= 64 || !((seen_s[e] >> (at & 63)) & 1ull)) x[e] = -INFINITY;
           }
         };
         auto above_m = [&](int r) { return *reinterpret_cast<const float4 *>(ref + r); };
@@ -393,13 +374,10 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
         // range: in bf16 past 2^8; in e4m3 past 448 (2^8.8), from 2^4 at the last
         // move, so that small weights keep their bits.
         constexpr float kRoom = kByte ? 8.8f : 8.0f, kAbove = kByte ? 4.0f : 0.0f;
-        float z[kT], top = -INFINITY;
+        float z[kRows], top = -INFINITY;
+        load(z, above_m);
 #pragma unroll
-        for (int c = 0; c < kT; c += 16) {
-          load(rb + c, z + c, above_m);
-#pragma unroll
-          for (int r = c; r < c + 16; ++r) top = fmaxf(top, z[r]);
-        }
+        for (int r = 0; r < kRows; ++r) top = fmaxf(top, z[r]);
         if (here > 0) idle(last_v);
         last_v = vi;
         tc_fence_before();
@@ -407,13 +385,10 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
         const bool speaks = (tid & (kGroup - 1)) == 0;
         if (speaks) mbar_arrive(empty + k_slot);  // K and its scales are read
         if (move) {
-#pragma unroll 1
-          for (int c = rb; c < rb + kT; c += 16) {
-            float v[16];
-            load(c, v, [&](int) { return make_float4(-lv, -lv, -lv, -lv); });
-            join_lanes<true>(v, lane);
-            if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + c + (lane >> 1)] = v[0];
-          }
+          float v[kRows];
+          load(v, [&](int) { return make_float4(-lv, -lv, -lv, -lv); });
+          join_lanes<true>(v, lane);
+          if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + (lane >> 1)] = v[0];
           named_barrier(bar_group, kGroup);
           const int r = tid & (kGroup - 1);
           if (r < kRows) {
@@ -424,21 +399,19 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
             fade[r] = next == m ? 1.0f : exp2_f(m - next);
           }
           named_barrier(bar_group, kGroup);
+          load(z, above_m);
 #pragma unroll
-          for (int c = 0; c < kT; c += 16) load(rb + c, z + c, above_m);
-#pragma unroll
-          for (int e = 0; e < kT; ++e) l[e] *= fade[rb + e];
+          for (int e = 0; e < kRows; ++e) l[e] *= fade[e];
           if (here > 0) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kN / L::kParts; c += 16) {
-              const int at = c + team % L::kParts * (kN / L::kParts);
-              float o[16];
-              tmem_ld<16>(tm_o + at, o);
-              tmem_wait_ld<16>(o);
+            for (int c = 0; c < kN; c += kRows) {
+              float o[kRows];
+              tmem_ld<kRows>(tm_o + c, o);
+              tmem_wait_ld<kRows>(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= fade[(at & (kRows - 1)) + e];
-              tmem_st<16>(tm_o + at, reinterpret_cast<const uint32_t *>(o));
+              for (int e = 0; e < kRows; ++e) o[e] *= fade[e];
+              tmem_st<kRows>(tm_o + c, reinterpret_cast<const uint32_t *>(o));
             }
             tmem_wait_st();
           }
@@ -449,11 +422,9 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
         // ---- weights ----
         uint8_t *mine = smem + L::kWeights + (s * 128 + t) * kRowBytes;
         // 16-byte vector c of a token's row under the swizzle of its span
-        auto swizzle = [&](int c) {
-          return (kRowBytes == 128 ? c ^ (t & 7) : kRowBytes == 64 ? c ^ ((t >> 1) & 3) : c ^ ((t >> 2) & 1)) << 4;
-        };
+        auto swizzle = [&](int c) { return (c ^ ((t >> 2) & 1)) << 4; };
 #pragma unroll
-        for (int r = 0; r < kT; r += kByte ? 16 : 8) {
+        for (int r = 0; r < kRows; r += kByte ? 16 : 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < (kByte ? 16 : 8); e += 4) {
@@ -471,18 +442,16 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
             }
           }
           if constexpr (kByte) {
-            *reinterpret_cast<uint4 *>(mine + swizzle((rb + r) >> 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(mine + swizzle((kRows + rb + r) >> 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(mine + swizzle(0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(mine + swizzle(1)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else {
-            *reinterpret_cast<uint4 *>(mine + swizzle((rb + r) >> 3)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(mine + swizzle(r >> 3)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           }
         }
         if (masked) {
-          constexpr int kVectors = (kByte ? 8 : 16) / L::kParts;
           wait(full + v_slot, (vi / kSlots) & 1);
           if (token >= first &&
-              clean_values<kByte>(smem + L::kRing + v_slot * L::kSlot, t, token >= g.len,
-                                  team % L::kParts * kVectors, (team % L::kParts + 1) * kVectors))
+              clean_values<kByte>(smem + L::kRing + v_slot * L::kSlot, t, token >= g.len, 0, kByte ? 8 : 16))
             *odd = 1;
         }
         ++count;
@@ -494,11 +463,8 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
 
       // ---- the end of a segment: the groups' sums and O together ----
       if (here > 0) idle(last_v);
-#pragma unroll
-      for (int c = 0; c < kT; c += 16) {
-        join_lanes<false>(l + c, lane);
-        if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + rb + c + (lane >> 1)] = l[c];
-      }
+      join_lanes<false>(l, lane);
+      if ((lane & 1) == 0) warp_row_s[(4 * s + w) * kRows + (lane >> 1)] = l[0];
       tc_fence_after();
       named_barrier(bar_all, kGroups * kGroup);
       const bool whole = g.tiles == g.all;
@@ -518,10 +484,10 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
       }
       named_barrier(bar_all, kGroups * kGroup);
       // four rows at a time, 32 channels a warp, one a lane
-      constexpr int kMine = kRows / (kGroups * L::kParts);
+      constexpr int kMine = kRows / kGroups;
       float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * p.rows * kPartialStride;
 #pragma unroll 1
-      for (int r0 = team * kMine; r0 < (team + 1) * kMine && (r0 >> p.group_log2) < g.size; r0 += 4) {
+      for (int r0 = s * kMine; r0 < (s + 1) * kMine && (r0 >> p.group_log2) < g.size; r0 += 4) {
         float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int u = 0; u < used; ++u) {
@@ -570,37 +536,29 @@ __global__ void __launch_bounds__(Narrow<kByte, kRows>::kThreads, 1)
   }
 }
 
-template <bool kByte, int kRows>
+template <bool kByte>
 cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
-  using L = Narrow<kByte, kRows>;
+  using L = Narrow<kByte>;
   static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
-    e = cudaFuncSetAttribute(tree_narrow_kernel<kByte, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    e = cudaFuncSetAttribute(tree_narrow_kernel<kByte>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_narrow_kernel<kByte, kRows><<<p.ctas, L::kThreads, L::kTotal, stream>>>(map_k, map_v, p);
+  tree_narrow_kernel<kByte><<<p.ctas, L::kThreads, L::kTotal, stream>>>(map_k, map_v, p);
   return cudaGetLastError();
-}
-
-template <bool kByte>
-cudaError_t launch_format(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, cudaStream_t stream) {
-  const int rows = p.nodes << p.group_log2;
-  if (rows <= 16) return launch_as<kByte, 16>(p, map_k, map_v, stream);
-  if (rows <= 32) return launch_as<kByte, 32>(p, map_k, map_v, stream);
-  return launch_as<kByte, 64>(p, map_k, map_v, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_narrow(const TreeParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
                                cudaStream_t stream) {
-  return p.format == FFD_CACHE_BYTE ? launch_format<true>(p, map_k, map_v, stream)
-                                    : launch_format<false>(p, map_k, map_v, stream);
+  return p.format == FFD_CACHE_BYTE ? launch_as<true>(p, map_k, map_v, stream)
+                                    : launch_as<false>(p, map_k, map_v, stream);
 }
 
 }  // namespace ffd
