@@ -15,7 +15,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowLanes = 16;                     // threads of a row, 8 channels (16 bytes) each
 constexpr int kRowsAtOnce = kThreads / kRowLanes;  // rows a block handles at a time
-constexpr int kMaxTokens = 4;                      // tokens of a block
+constexpr int kMaxTokens = 8;                      // tokens of a block
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -40,27 +40,72 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
   return len - count + i;
 }
 
-// A block takes kTokens tokens and the row chunk blockIdx.y of each.
+// A block takes `tokens_a_block` tokens and the row chunk blockIdx.y of each, at
+// most kTableRows rows.
 //
 // The angles come first: thread t finds (cos, sin) of one pair of one token
 // and leaves them in shared memory, since every head of the token needs them.
 // position * turns wraps at whole turns in 64 bits; its top 32 bits, signed,
-// are the angle in turns to 2^-32, and sincospif takes it from there.
+// are the angle in turns to 2^-32, and sincospif takes it from there.  Thread t
+// also finds where row t comes from and goes to, once instead of 16 times.
 //
-// Then 16 threads take a row.  Where the pairs' halves fall on whole threads
-// (rotary_dim a multiple of 16, or interleaved) the partner channels come by
-// shuffle; else each partner is loaded on its own.
+// Then 16 threads take a row, kInFlight rows each before the first is used: a
+// block has 16 KB on its way from HBM.  Where the pairs' halves fall on whole
+// threads (rotary_dim a multiple of 16, or interleaved) the partner channels
+// come by shuffle; else each partner is loaded on its own.
 //
 // E4M3: the row's largest magnitude is found on the bit patterns (as unsigned
 // integers they order like the values, with NaN above infinity).
+constexpr int kInFlight = 4;
+constexpr int kTableRows = kThreads;
+
+struct RowPlace {
+  const uint16_t *src;
+  uint8_t *dst;       // null: not written
+};
+
 template <bool kAppend, bool kByte>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsParams p, int tokens_a_block,
                                                         int rows_a_block) {
   extern __shared__ float2 turn_s[];  // [tokens_a_block][half]
-  __shared__ int seq_s[kMaxTokens], slot_s[kMaxTokens];
+  __shared__ RowPlace place_s[kTableRows];
+  __shared__ uint16_t *scale_s[kByte ? kTableRows : 1];
+  __shared__ uint16_t kind_s[kTableRows];  // token of the block * 4 + (0 query, 1 key, 2 value)
   const int half = p.rotary_dim >> 1;
   const int token0 = blockIdx.x * tokens_a_block;
   const int tokens_here = min(tokens_a_block, p.tokens - token0);
+  const int kv_rows = p.k != nullptr ? p.kv_heads : 0;
+  const int q_rows = p.q != nullptr ? p.q_heads : 0;
+  const int rows = q_rows + kv_rows + (kAppend ? kv_rows : 0);
+  const int row_begin = blockIdx.y * rows_a_block;
+  const int width = min(rows, row_begin + rows_a_block) - row_begin;
+  const int todo = tokens_here * width;
+  if (static_cast<int>(threadIdx.x) < todo) {
+    const int tl = threadIdx.x / width, row = row_begin + threadIdx.x - tl * width;
+    const int token = token0 + tl;
+    const int kind = row < q_rows ? 0 : row < q_rows + kv_rows ? 1 : 2;
+    const int head = kind == 0 ? row : (row - q_rows) - (kind == 2 ? kv_rows : 0);
+    RowPlace at;
+    at.src = kind == 0 ? p.q + (static_cast<size_t>(token) * q_rows + head) * kHeadDim
+                       : (kind == 1 ? p.k : p.v) + (static_cast<size_t>(token) * kv_rows + head) * kHeadDim;
+    int slot = 0, b = 0;
+    if (kAppend) {
+      b = token / p.new_tokens;
+      slot = token_slot(p, b, token - b * p.new_tokens);
+    }
+    if (kind == 0) {
+      at.dst = reinterpret_cast<uint8_t *>(p.q_out + (static_cast<size_t>(token) * q_rows + head) * kHeadDim);
+    } else if (kAppend) {
+      const size_t to = (static_cast<size_t>(b) * p.kv_heads + head) * p.capacity + slot;
+      at.dst = static_cast<uint8_t *>(kind == 1 ? p.k_out : p.v_out) + to * (kByte ? kByteRow : 2 * kHeadDim);
+      if (kByte) scale_s[threadIdx.x] = (kind == 1 ? p.k_scales : p.v_scales) + to;
+    } else {
+      at.dst = static_cast<uint8_t *>(p.k_out) + (static_cast<size_t>(token) * kv_rows + head) * (2 * kHeadDim);
+    }
+    if (slot < 0) at.dst = nullptr;
+    place_s[threadIdx.x] = at;
+    kind_s[threadIdx.x] = static_cast<uint16_t>(4 * tl + kind);
+  }
   for (int t = threadIdx.x; t < tokens_here * half; t += kThreads) {
     const int tl = t / half, token = token0 + tl;
     int position;
@@ -75,182 +120,164 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     sincospif(static_cast<float>(static_cast<int32_t>(wrapped >> 32)) * 0x1p-31f, &sine, &cosine);
     turn_s[t] = make_float2(cosine * p.amplitude, sine * p.amplitude * p.sign);
   }
-  if (kAppend && static_cast<int>(threadIdx.x) < tokens_here) {
-    const int token = token0 + threadIdx.x, b = token / p.new_tokens;
-    seq_s[threadIdx.x] = b;
-    slot_s[threadIdx.x] = token_slot(p, b, token - b * p.new_tokens);
-  }
   __syncthreads();
 
   const int lane = threadIdx.x & (kRowLanes - 1);
-  const int kv_rows = p.k != nullptr ? p.kv_heads : 0;
-  const int q_rows = p.q != nullptr ? p.q_heads : 0;
-  const int rows = q_rows + kv_rows + (kAppend ? kv_rows : 0);
-  const int row_begin = blockIdx.y * rows_a_block;
-  const int row_end = min(rows, row_begin + rows_a_block);
-  const int width = row_end - row_begin;
-  const int todo = tokens_here * width;
+  const int c0 = 8 * lane;
   // (every thread of a warp runs the same number of rounds: the shuffles need both halves)
-  for (int at = 0; at < todo; at += kRowsAtOnce) {
-    const int mine = at + static_cast<int>(threadIdx.x) / kRowLanes;
-    bool live = mine < todo;
-    const int tl = live ? mine / width : 0;
-    const int row = row_begin + (live ? mine - tl * width : 0);
-    const size_t token = token0 + tl;
-    int slot = 0, b = 0;
-    if (kAppend) {
-      b = seq_s[tl];
-      slot = slot_s[tl];
-      live = live && slot >= 0;
+  for (int at = 0; at < todo; at += kInFlight * kRowsAtOnce) {
+    uint4 loaded[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int mine = at + u * kRowsAtOnce + static_cast<int>(threadIdx.x) / kRowLanes;
+      loaded[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine < todo && place_s[mine].dst != nullptr)
+        loaded[u] = *reinterpret_cast<const uint4 *>(place_s[mine].src + c0);
     }
-    const int kind = row < q_rows ? 0 : row < q_rows + kv_rows ? 1 : 2;
-    const int head = kind == 0 ? row : (row - q_rows) - (kind == 2 ? kv_rows : 0);
-    const uint16_t *src = kind == 0 ? p.q + (token * q_rows + head) * kHeadDim
-                                    : (kind == 1 ? p.k : p.v) + (token * kv_rows + head) * kHeadDim;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (live) w = *reinterpret_cast<const uint4 *>(src + 8 * lane);
-    float x[8];
-    unpack8(w, x);
-    const float2 *cs = turn_s + tl * half;
-    const int c0 = 8 * lane;
-    if (half > 0 && p.interleaved) {
-      if (kind != 2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = (c0 >> 1) + e;
-          if (i < half) {
-            const float2 t = cs[i];
-            const float u = x[2 * e], v = x[2 * e + 1];
-            x[2 * e] = u * t.x - v * t.y;
-            x[2 * e + 1] = v * t.x + u * t.y;
-          }
-        }
-      }
-    } else if (half > 0 && (half & 7) == 0) {
-      const int step = half >> 3;  // threads between a pair's halves
-      const bool first = lane < step, second = !first && lane < 2 * step;
-      const int from = first ? lane + step : second ? lane - step : lane;
-      uint4 o;
-      o.x = __shfl_sync(0xFFFFFFFFu, w.x, from, kRowLanes);
-      o.y = __shfl_sync(0xFFFFFFFFu, w.y, from, kRowLanes);
-      o.z = __shfl_sync(0xFFFFFFFFu, w.z, from, kRowLanes);
-      o.w = __shfl_sync(0xFFFFFFFFu, w.w, from, kRowLanes);
-      if (kind != 2 && (first || second)) {
-        float y[8];
-        unpack8(o, y);
-        const float2 *t = cs + (first ? c0 : c0 - half);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + (first ? -y[e] : y[e]) * t[e].y;
-      }
-    } else if (half > 0 && kind != 2 && live) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = c0 + e;
-        if (c < half) {
-          x[e] = x[e] * cs[c].x - lo_f(src[c + half]) * cs[c].y;
-        } else if (c < 2 * half) {
-          x[e] = x[e] * cs[c - half].x + lo_f(src[c - half]) * cs[c - half].y;
-        }
-      }
-    }
-    __syncwarp();  // (an output may be its input: every partner is read before any store)
-    if (!kByte || kind == 0) {
-      const uint4 y = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                 pack_bf16(x[6], x[7]));
-      uint16_t *dst;
-      if (kind == 0) {
-        dst = p.q_out + (token * q_rows + head) * kHeadDim;
-      } else if (kAppend) {
-        dst = static_cast<uint16_t *>(kind == 1 ? p.k_out : p.v_out) +
-              ((static_cast<size_t>(b) * p.kv_heads + head) * p.capacity + slot) * kHeadDim;
-      } else {
-        dst = static_cast<uint16_t *>(p.k_out) + (token * kv_rows + head) * kHeadDim;
-      }
-      if (live) *reinterpret_cast<uint4 *>(dst + c0) = y;
-    }
-    if (kByte) {
-      uint32_t top = 0u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int d = kRowLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d, kRowLanes));
-      if (live && kind != 0) {
-        const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 448.0f));
-        const float s = __bfloat162float(s16);
-        uint16_t s_bits = __bfloat16_as_ushort(s16);
-        uint32_t codes[2] = {0u, 0u};
-        if (top >= 0x7F800000u) {
-          s_bits = 0x7FFFu;
-          codes[0] = codes[1] = 0x7F7F7F7Fu;
-        } else if (s != 0.0f) {
+    for (int u = 0; u < kInFlight; ++u) {
+      if (at + u * kRowsAtOnce >= todo) break;
+      const int mine = at + u * kRowsAtOnce + static_cast<int>(threadIdx.x) / kRowLanes;
+      const bool there = mine < todo;
+      const RowPlace place = place_s[there ? mine : 0];
+      const int what = kind_s[there ? mine : 0], kind = what & 3;
+      const bool live = there && place.dst != nullptr;
+      const uint4 w = loaded[u];
+      float x[8];
+      unpack8(w, x);
+      const float2 *cs = turn_s + (what >> 2) * half;
+      if (half > 0 && p.interleaved) {
+        if (kind != 2) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 y = make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
-            codes[e >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
-                             << (16 * (e & 1));
+            const int i = (c0 >> 1) + e;
+            if (i < half) {
+              const float2 t = cs[i];
+              const float a = x[2 * e], b = x[2 * e + 1];
+              x[2 * e] = a * t.x - b * t.y;
+              x[2 * e + 1] = b * t.x + a * t.y;
+            }
           }
         }
-        const size_t at_row = (static_cast<size_t>(b) * p.kv_heads + head) * p.capacity + slot;
-        uint8_t *dst = static_cast<uint8_t *>(kind == 1 ? p.k_out : p.v_out) + at_row * kByteRow;
-        *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(codes[0], codes[1]);
-        if (lane == 0) (kind == 1 ? p.k_scales : p.v_scales)[at_row] = s_bits;
+      } else if (half > 0 && (half & 7) == 0) {
+        const int step = half >> 3;  // threads between a pair's halves
+        const bool first = lane < step, second = !first && lane < 2 * step;
+        const int from = first ? lane + step : second ? lane - step : lane;
+        uint4 o;
+        o.x = __shfl_sync(0xFFFFFFFFu, w.x, from, kRowLanes);
+        o.y = __shfl_sync(0xFFFFFFFFu, w.y, from, kRowLanes);
+        o.z = __shfl_sync(0xFFFFFFFFu, w.z, from, kRowLanes);
+        o.w = __shfl_sync(0xFFFFFFFFu, w.w, from, kRowLanes);
+        if (kind != 2 && (first || second)) {
+          float y[8];
+          unpack8(o, y);
+          const float2 *t = cs + (first ? c0 : c0 - half);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + (first ? -y[e] : y[e]) * t[e].y;
+        }
+      } else if (half > 0 && kind != 2 && live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = c0 + e;
+          if (c < half) {
+            x[e] = x[e] * cs[c].x - lo_f(place.src[c + half]) * cs[c].y;
+          } else if (c < 2 * half) {
+            x[e] = x[e] * cs[c - half].x + lo_f(place.src[c - half]) * cs[c - half].y;
+          }
+        }
+      }
+      __syncwarp();  // (an output may be its input: every partner is read before any store)
+      if (live && (!kByte || kind == 0))
+        *reinterpret_cast<uint4 *>(place.dst + 2 * c0) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      if (kByte) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int d = kRowLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d, kRowLanes));
+        if (live && kind != 0) {
+          const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 448.0f));
+          const float s = __bfloat162float(s16);
+          uint16_t s_bits = __bfloat16_as_ushort(s16);
+          uint32_t codes[2] = {0u, 0u};
+          if (top >= 0x7F800000u) {
+            s_bits = 0x7FFFu;
+            codes[0] = codes[1] = 0x7F7F7F7Fu;
+          } else if (s != 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
+              codes[e >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
+                               << (16 * (e & 1));
+            }
+          }
+          *reinterpret_cast<uint2 *>(place.dst + c0) = make_uint2(codes[0], codes[1]);
+          if (lane == 0) *scale_s[mine] = s_bits;
+        }
       }
     }
   }
 }
 
-// Eight codes (8 bytes in, 16 out) a thread; code * scale is exact in fp32 (4
-// and 8 significant bits), so the only rounding is the one to bf16.
-constexpr int kReadRows = 4;  // rows a thread has in flight
+// Sixteen codes (16 bytes in, 32 out) a thread and row; code * scale is exact in
+// fp32 (4 and 8 significant bits), so the only rounding is the one to bf16.
+constexpr int kReadRows = 4;   // rows a thread has in flight
+constexpr int kReadLanes = 8;  // threads of a row
+constexpr int kReadAtOnce = kThreads / kReadLanes;
 
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
   const int which = blockIdx.y;
   uint16_t *out = p.out[which];
   if (out == nullptr) return;
-  const int rows_a_block = kRowsAtOnce * kReadRows;
+  const int rows_a_block = kReadAtOnce * kReadRows;
   const int chunks = (p.count + rows_a_block - 1) / rows_a_block;
   const int bh = blockIdx.x / chunks;
   const int len = p.lengths[bh / p.kv_heads];
   if (len < 0 || len > p.capacity) return;
   const int rows = min(p.count, len - p.begin);
-  const int lane = threadIdx.x & (kRowLanes - 1);
-  const int first = (blockIdx.x - bh * chunks) * rows_a_block + threadIdx.x / kRowLanes;
+  const int lane = threadIdx.x & (kReadLanes - 1);
+  const int first = (blockIdx.x - bh * chunks) * rows_a_block + threadIdx.x / kReadLanes;
   const size_t in0 = static_cast<size_t>(bh) * p.capacity + p.begin;
   const size_t out0 = static_cast<size_t>(bh) * p.count;
-  uint2 w[kReadRows];
+  uint4 w[kReadRows];
   float s[kReadRows];
 #pragma unroll
   for (int r = 0; r < kReadRows; ++r) {
-    const int t = first + r * kRowsAtOnce;
+    const int t = first + r * kReadAtOnce;
     if (t < rows) {
-      w[r] = __ldcs(reinterpret_cast<const uint2 *>(p.codes[which] + (in0 + t) * kByteRow) + lane);
+      w[r] = __ldcs(reinterpret_cast<const uint4 *>(p.codes[which] + (in0 + t) * kByteRow) + lane);
       s[r] = lo_f(p.scales[which][in0 + t]);
     }
   }
 #pragma unroll
   for (int r = 0; r < kReadRows; ++r) {
-    const int t = first + r * kRowsAtOnce;
+    const int t = first + r * kReadAtOnce;
     if (t >= rows) continue;
-    uint32_t y[4];
+    const uint32_t words[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+    uint32_t y[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_fp8x2_storage_t pair =
-          static_cast<__nv_fp8x2_storage_t>(((e & 2) ? w[r].y : w[r].x) >> (16 * (e & 1)));
+    for (int e = 0; e < 8; ++e) {
+      const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>(words[e >> 1] >> (16 * (e & 1)));
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
       y[e] = pack_bf16(f.x * s[r], f.y * s[r]);
     }
-    __stcs(reinterpret_cast<uint4 *>(out + (out0 + t) * kHeadDim) + lane, make_uint4(y[0], y[1], y[2], y[3]));
+    uint4 *dst = reinterpret_cast<uint4 *>(out + (out0 + t) * kHeadDim) + 2 * lane;
+    __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
+    __stcs(dst + 1, make_uint4(y[4], y[5], y[6], y[7]));
   }
 }
 
 template <bool kAppend, bool kByte>
 cudaError_t launch_rows_as(const RowsParams &p, cudaStream_t stream) {
   const int rows = (p.q != nullptr ? p.q_heads : 0) + (p.k != nullptr ? (kAppend ? 2 : 1) * p.kv_heads : 0);
+  // Few tokens: as many blocks as there are sixteens of rows, for the latency.
+  // Many: whole tokens, whose angles are then found once.
   int tokens_a_block = 1, rows_a_block = kRowsAtOnce;
   if (p.tokens >= 2048) {
-    tokens_a_block = kMaxTokens;
-    rows_a_block = rows;
+    rows_a_block = rows < kTableRows ? rows : kTableRows;
+    while (tokens_a_block < kMaxTokens && 2 * tokens_a_block * rows_a_block <= kTableRows) tokens_a_block *= 2;
   }
   const dim3 grid(static_cast<unsigned>((p.tokens + tokens_a_block - 1) / tokens_a_block),
                   static_cast<unsigned>((rows + rows_a_block - 1) / rows_a_block));
@@ -267,7 +294,7 @@ cudaError_t launch_rows(const RowsParams &p, bool append, int format, cudaStream
 }
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream) {
-  const int rows = kRowsAtOnce * kReadRows;
+  const int rows = kReadAtOnce * kReadRows;
   const dim3 grid(static_cast<unsigned>((p.count + rows - 1) / rows) * static_cast<unsigned>(p.batch * p.kv_heads), 2);
   read_kernel<<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();

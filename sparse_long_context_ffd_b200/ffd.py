@@ -212,10 +212,11 @@ def load_library() -> ctypes.CDLL:
             lib.ffd_check_device_status.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), p]
             lib.ffd_check_device_status.restype = st
             lib.ffd_rope_init.argtypes = [ctypes.POINTER(_RopeOptions), ctypes.POINTER(Rope)]
-            lib.ffd_rotate.argtypes = [p, ctypes.c_int64, p, i32, i32, p, p, i32, p, p, p]
-            lib.ffd_append_tokens.argtypes = [sp, p, p, i32, p, p, p, p, p, p, p, p]
-            lib.ffd_read_cache.argtypes = [sp, p, p, i32, i32, p, p, p]
-            lib.ffd_decode_tree.argtypes = [sp, p, i32, p, p, p, p, p, p, sz, p]
+            rp, cp = ctypes.POINTER(Rope), ctypes.POINTER(_Cache)
+            lib.ffd_rotate.argtypes = [rp, ctypes.c_int64, p, i32, i32, p, p, i32, p, p, p]
+            lib.ffd_append_tokens.argtypes = [sp, cp, rp, i32, p, p, p, p, p, p, p, p]
+            lib.ffd_read_cache.argtypes = [sp, cp, p, i32, i32, p, p, p]
+            lib.ffd_decode_tree.argtypes = [sp, cp, i32, p, p, p, p, p, p, sz, p]
             lib.ffd_decode_tree_workspace_bytes.argtypes = [sp, i32]
             lib.ffd_decode_tree_workspace_bytes.restype = sz
             lib.ffd_decode_tree_workspace_init.argtypes = [sp, i32, p, sz, p]
@@ -471,13 +472,37 @@ def check_device_status(workspace, stream=None) -> int:
 # and launch on the tensors' device: on its current stream unless one is given.
 
 
+class _Entry:
+    """What these wrappers ask torch and the library for on every call, looked
+    up once: a call costs the host a few microseconds in all."""
+
+    def __init__(self):
+        import torch
+        self.bf16, self.i32, self.i64 = torch.bfloat16, torch.int32, torch.int64
+        self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.use_device = torch.cuda.device
+        lib = load_library()
+        self.rotate, self.append_tokens = lib.ffd_rotate, lib.ffd_append_tokens
+        self.read_cache, self.decode_tree = lib.ffd_read_cache, lib.ffd_decode_tree
+
+
+_the_entry: Optional[_Entry] = None
+
+
+def _entry() -> _Entry:
+    global _the_entry
+    if _the_entry is None:
+        _the_entry = _Entry()
+    return _the_entry
+
+
 def _tensor(t, dtype, shape, what: str, device: int) -> int:
     """Data pointer of a dense CUDA tensor of exactly this type, shape and device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
 def _device_of(t) -> int:
@@ -488,15 +513,15 @@ def _device_of(t) -> int:
 
 def _call(device: int, stream, what: str, fn, *args) -> None:
     """fn(*args, stream) with `device` current."""
-    import torch
+    e = _entry()
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
+        stream = e.raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == device:
+    if e.device() == device:
         status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with e.use_device(device):
             status = fn(*args, stream)
     if status != FFD_OK:
         raise FFDError(status, what)
@@ -522,7 +547,6 @@ class KVCache:
                          _tensor(v, k.dtype, k.shape, "v", device),
                          None if k_scales is None else _tensor(k_scales, torch.bfloat16, s, "k_scales", device),
                          None if v_scales is None else _tensor(v_scales, torch.bfloat16, s, "v_scales", device))
-        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, shape: Shape, format: int = FFD_CACHE_BF16, device="cuda"):
@@ -539,7 +563,7 @@ class KVCache:
     def _of(self, shape: Shape):
         if self.key != (shape.batch, shape.num_kv_heads, shape.capacity):
             raise ValueError(f"cache {self.key} does not fit {shape}")
-        return self._ref
+        return self._c
 
 
 def rotate(rope: Rope, positions, q, q_out, k=None, k_out=None, inverse: bool = False,
@@ -547,23 +571,23 @@ def rotate(rope: Rope, positions, q, q_out, k=None, k_out=None, inverse: bool = 
     """ffd_rotate: rotary positions of bf16 q [tokens, Hq, 128] and, if given,
     k [tokens, Hkv, 128]; positions int32 [tokens].  An output may be its
     input."""
-    import torch
-    dev, bf16 = _device_of(q), torch.bfloat16
-    if q.dim() != 3 or q.shape[2] != 128:
+    e, dev, shape = _entry(), _device_of(q), q.shape
+    if len(shape) != 3 or shape[2] != 128:
         raise ValueError("q is [tokens, heads, 128]")
-    tokens = q.shape[0]
+    tokens = shape[0]
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    args = (ctypes.byref(rope), tokens, _tensor(positions, torch.int32, torch.Size((tokens,)), "positions", dev),
-            1 if inverse else 0, q.shape[1], _tensor(q, bf16, q.shape, "q", dev),
-            _tensor(q_out, bf16, q.shape, "q_out", dev))
     if k is None:
-        args += (0, None, None)
+        heads, k_at, k_out_at = 0, None, None
     else:
-        if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != 128:
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != tokens or k_shape[2] != 128:
             raise ValueError("k is [tokens, heads, 128]")
-        args += (k.shape[1], _tensor(k, bf16, k.shape, "k", dev), _tensor(k_out, bf16, k.shape, "k_out", dev))
-    _call(dev, stream, "ffd_rotate", load_library().ffd_rotate, *args)
+        heads = k_shape[1]
+        k_at, k_out_at = _tensor(k, e.bf16, k_shape, "k", dev), _tensor(k_out, e.bf16, k_shape, "k_out", dev)
+    _call(dev, stream, "ffd_rotate", e.rotate, rope, tokens,
+          _tensor(positions, e.i32, (tokens,), "positions", dev), 1 if inverse else 0, shape[1],
+          _tensor(q, e.bf16, shape, "q", dev), _tensor(q_out, e.bf16, shape, "q_out", dev), heads, k_at, k_out_at)
 
 
 def append_tokens(shape: Shape, cache: KVCache, k_new, v_new, lengths, rope: Optional[Rope] = None,
@@ -573,20 +597,18 @@ def append_tokens(shape: Shape, cache: KVCache, k_new, v_new, lengths, rope: Opt
     q, q_out bf16 [B, n, Hq, 128] or neither; lengths int32 [B], the new tokens
     counted; new_lengths int32 [B] for fewer than n; positions int32 [B, n]
     (default: the slots)."""
-    import torch
-    dev, bf16, i32, size = cache.device, torch.bfloat16, torch.int32, torch.Size
-    B, n = shape.batch, k_new.shape[1]
-    kv = size((B, n, shape.num_kv_heads, 128))
+    e, dev = _entry(), cache.device
+    bf16, i32, B, n = e.bf16, e.i32, shape.batch, k_new.shape[1]
+    kv = (B, n, shape.num_kv_heads, 128)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    qs = size((B, n, shape.num_q_heads, 128))
-    _call(dev, stream, "ffd_append_tokens", load_library().ffd_append_tokens, ctypes.byref(shape),
-          cache._of(shape), None if rope is None else ctypes.byref(rope), n,
+    qs = (B, n, shape.num_q_heads, 128)
+    _call(dev, stream, "ffd_append_tokens", e.append_tokens, shape, cache._of(shape), rope, n,
           None if q is None else _tensor(q, bf16, qs, "q", dev), _tensor(k_new, bf16, kv, "k_new", dev),
           _tensor(v_new, bf16, kv, "v_new", dev),
-          None if positions is None else _tensor(positions, i32, size((B, n)), "positions", dev),
-          _tensor(lengths, i32, size((B,)), "lengths", dev),
-          None if new_lengths is None else _tensor(new_lengths, i32, size((B,)), "new_lengths", dev),
+          None if positions is None else _tensor(positions, i32, (B, n), "positions", dev),
+          _tensor(lengths, i32, (B,), "lengths", dev),
+          None if new_lengths is None else _tensor(new_lengths, i32, (B,), "new_lengths", dev),
           None if q_out is None else _tensor(q_out, bf16, qs, "q_out", dev))
 
 
@@ -594,17 +616,15 @@ def read_cache(shape: Shape, cache: KVCache, lengths, token_begin: int, k_out=No
                stream=None) -> None:
     """ffd_read_cache: tokens from token_begin on of an 8-bit cache back to
     bf16; k_out, v_out [B, Hkv, count, 128], either may be None."""
-    import torch
     if k_out is None and v_out is None:
         raise ValueError("nothing to read: k_out and v_out are None")
+    e, dev = _entry(), cache.device
     count = (k_out if k_out is not None else v_out).shape[2]
-    want = torch.Size((shape.batch, shape.num_kv_heads, count, 128))
-    dev = cache.device
-    _call(dev, stream, "ffd_read_cache", load_library().ffd_read_cache, ctypes.byref(shape),
-          cache._of(shape), _tensor(lengths, torch.int32, torch.Size((shape.batch,)), "lengths", dev),
-          int(token_begin), count,
-          None if k_out is None else _tensor(k_out, torch.bfloat16, want, "k_out", dev),
-          None if v_out is None else _tensor(v_out, torch.bfloat16, want, "v_out", dev))
+    want = (shape.batch, shape.num_kv_heads, count, 128)
+    _call(dev, stream, "ffd_read_cache", e.read_cache, shape, cache._of(shape),
+          _tensor(lengths, e.i32, (shape.batch,), "lengths", dev), int(token_begin), count,
+          None if k_out is None else _tensor(k_out, e.bf16, want, "k_out", dev),
+          None if v_out is None else _tensor(v_out, e.bf16, want, "v_out", dev))
 
 
 def decode_tree_workspace_bytes(shape: Shape, num_nodes: int) -> int:
@@ -631,17 +651,17 @@ def decode_tree(shape: Shape, cache: KVCache, q, lengths, out, workspace, tree_m
     int32 [B], the tree counted; tree_mask int64 [B, n] (bit j of node i's
     word: i sees j; default a chain); tree_sizes int32 [B] for fewer than n
     nodes.  tree_from_parents makes masks from parent lists."""
-    import torch
-    dev, bf16, size = cache.device, torch.bfloat16, torch.Size
+    e, dev = _entry(), cache.device
     B, n = shape.batch, q.shape[1]
-    qs = size((B, n, shape.num_q_heads, 128))
-    _call(dev, stream, "ffd_decode_tree", load_library().ffd_decode_tree, ctypes.byref(shape),
-          cache._of(shape), n, _tensor(q, bf16, qs, "q", dev),
-          _tensor(lengths, torch.int32, size((B,)), "lengths", dev),
-          None if tree_sizes is None else _tensor(tree_sizes, torch.int32, size((B,)), "tree_sizes", dev),
-          None if tree_mask is None else _tensor(tree_mask, torch.int64, size((B, n)), "tree_mask", dev),
-          _tensor(out, bf16, qs, "out", dev),
-          _tensor(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel())
+    qs = (B, n, shape.num_q_heads, 128)
+    if workspace.dim() != 1 or workspace.element_size() != 1:
+        raise ValueError("workspace: the bytes that tree_workspace gives")
+    nbytes = workspace.numel()
+    _call(dev, stream, "ffd_decode_tree", e.decode_tree, shape, cache._of(shape), n,
+          _tensor(q, e.bf16, qs, "q", dev), _tensor(lengths, e.i32, (B,), "lengths", dev),
+          None if tree_sizes is None else _tensor(tree_sizes, e.i32, (B,), "tree_sizes", dev),
+          None if tree_mask is None else _tensor(tree_mask, e.i64, (B, n), "tree_mask", dev),
+          _tensor(out, e.bf16, qs, "out", dev), _tensor(workspace, workspace.dtype, (nbytes,), "workspace", dev), nbytes)
 
 
 def tree_from_parents(parents):
