@@ -20,6 +20,12 @@ constexpr int kMaxTokens = 8;                      // tokens of a block
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -49,13 +55,13 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
 // are the angle in turns to 2^-32, and sincospif takes it from there.  Thread t
 // also finds where row t comes from and goes to, once instead of 16 times.
 //
-// Then 16 threads take a row, kInFlight rows each before the first is used: a
-// block has 16 KB on its way from HBM.  Where the pairs' halves fall on whole
+// Then 16 threads take rows of one token, kInFlight before the first is used (a
+// block has 16 KB on its way from HBM), each with the angles of its channels in
+// registers: read from shared memory at every row, they were 88% of its
+// bandwidth and set the pace.  Where the pairs' halves fall on whole
 // threads (rotary_dim a multiple of 16, or interleaved) the partner channels
 // come by shuffle; else each partner is loaded on its own.
 //
-// E4M3: the row's largest magnitude is found on the bit patterns (as unsigned
-// integers they order like the values, with NaN above infinity).
 constexpr int kInFlight = 4;
 constexpr int kTableRows = kThreads;
 
@@ -65,12 +71,12 @@ struct RowPlace {
 };
 
 template <bool kAppend, bool kByte>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowsParams p, int tokens_a_block,
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant__ RowsParams p, int tokens_a_block,
                                                         int rows_a_block) {
   extern __shared__ float2 turn_s[];  // [tokens_a_block][half]
   __shared__ RowPlace place_s[kTableRows];
   __shared__ uint16_t *scale_s[kByte ? kTableRows : 1];
-  __shared__ uint16_t kind_s[kTableRows];  // token of the block * 4 + (0 query, 1 key, 2 value)
+  __shared__ uint8_t kind_s[kTableRows];  // 0 query, 1 key, 2 value
   const int half = p.rotary_dim >> 1;
   const int token0 = blockIdx.x * tokens_a_block;
   const int tokens_here = min(tokens_a_block, p.tokens - token0);
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     }
     if (slot < 0) at.dst = nullptr;
     place_s[threadIdx.x] = at;
-    kind_s[threadIdx.x] = static_cast<uint16_t>(4 * tl + kind);
+    kind_s[threadIdx.x] = static_cast<uint8_t>(kind);
   }
   for (int t = threadIdx.x; t < tokens_here * half; t += kThreads) {
     const int tl = t / half, token = token0 + tl;
@@ -124,44 +130,59 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 
   const int lane = threadIdx.x & (kRowLanes - 1);
   const int c0 = 8 * lane;
+  const int mine_token = (threadIdx.x / kRowLanes) % tokens_a_block;  // tokens_a_block: a power of two up to 16
+  const int first_row = threadIdx.x / kRowLanes / tokens_a_block, row_step = kRowsAtOnce / tokens_a_block;
+  const float2 *cs = turn_s + mine_token * half;
+  // the pairs of this thread's channels: 8 of them, or (interleaved) 4
+  const int step = half >> 3;  // half layout: threads between a pair's halves
+  const bool first = lane < step, second = !first && lane < 2 * step;
+  float2 turn[8];
+  if (mine_token < tokens_here) {
+    if (p.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((c0 >> 1) + e < half) turn[e] = cs[(c0 >> 1) + e];
+    } else if ((half & 7) == 0 && (first || second)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        turn[e] = cs[(first ? c0 : c0 - half) + e];
+        if (first) turn[e].y = -turn[e].y;
+      }
+    }
+  }
   // (every thread of a warp runs the same number of rounds: the shuffles need both halves)
-  for (int at = 0; at < todo; at += kInFlight * kRowsAtOnce) {
+  for (int at = 0; at < width; at += kInFlight * row_step) {
     uint4 loaded[kInFlight];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-      const int mine = at + u * kRowsAtOnce + static_cast<int>(threadIdx.x) / kRowLanes;
+      const int row = at + u * row_step + first_row, mine = mine_token * width + row;
       loaded[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (mine < todo && place_s[mine].dst != nullptr)
+      if (row < width && mine < todo && place_s[mine].dst != nullptr)
         loaded[u] = *reinterpret_cast<const uint4 *>(place_s[mine].src + c0);
     }
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-      if (at + u * kRowsAtOnce >= todo) break;
-      const int mine = at + u * kRowsAtOnce + static_cast<int>(threadIdx.x) / kRowLanes;
-      const bool there = mine < todo;
+      if (at + u * row_step >= width) break;
+      const int row = at + u * row_step + first_row, mine = mine_token * width + row;
+      const bool there = row < width && mine < todo;
       const RowPlace place = place_s[there ? mine : 0];
-      const int what = kind_s[there ? mine : 0], kind = what & 3;
+      const int kind = kind_s[there ? mine : 0];
       const bool live = there && place.dst != nullptr;
       const uint4 w = loaded[u];
       float x[8];
       unpack8(w, x);
-      const float2 *cs = turn_s + (what >> 2) * half;
       if (half > 0 && p.interleaved) {
         if (kind != 2) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = (c0 >> 1) + e;
-            if (i < half) {
-              const float2 t = cs[i];
+            if ((c0 >> 1) + e < half) {
               const float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = a * t.x - b * t.y;
-              x[2 * e + 1] = b * t.x + a * t.y;
+              x[2 * e] = a * turn[e].x - b * turn[e].y;
+              x[2 * e + 1] = b * turn[e].x + a * turn[e].y;
             }
           }
         }
       } else if (half > 0 && (half & 7) == 0) {
-        const int step = half >> 3;  // threads between a pair's halves
-        const bool first = lane < step, second = !first && lane < 2 * step;
         const int from = first ? lane + step : second ? lane - step : lane;
         uint4 o;
         o.x = __shfl_sync(0xFFFFFFFFu, w.x, from, kRowLanes);
@@ -171,9 +192,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         if (kind != 2 && (first || second)) {
           float y[8];
           unpack8(o, y);
-          const float2 *t = cs + (first ? c0 : c0 - half);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + (first ? -y[e] : y[e]) * t[e].y;
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * turn[e].x + y[e] * turn[e].y;
         }
       } else if (half > 0 && kind != 2 && live) {
 #pragma unroll
@@ -191,26 +211,42 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         *reinterpret_cast<uint4 *>(place.dst + 2 * c0) =
             make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
       if (kByte) {
-        uint32_t top = 0u;
+        if (__all_sync(0xFFFFFFFFu, kind == 0)) continue;
+        float top = 0.0f;  // (the maximum of a row with a NaN in it is NaN)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
 #pragma unroll
-        for (int d = kRowLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d, kRowLanes));
+        for (int d = kRowLanes / 2; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d, kRowLanes));
         if (live && kind != 0) {
-          const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 448.0f));
+          const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(top, 448.0f));
           const float s = __bfloat162float(s16);
           uint16_t s_bits = __bfloat16_as_ushort(s16);
           uint32_t codes[2] = {0u, 0u};
-          if (top >= 0x7F800000u) {
+          if (!(top < INFINITY)) {
             s_bits = 0x7FFFu;
             codes[0] = codes[1] = 0x7F7F7F7Fu;
           } else if (s != 0.0f) {
+            // x / s correctly rounded, by Markstein's theorem (IBM J. Res. Dev. 34,
+            // 1990): with inv the correctly rounded 1 / s, q = x inv and the exact
+            // remainder x - q s, q + remainder inv is the rounded quotient, as long
+            // as nothing underflows.  (A quotient below 2^-11 has code 0 anyway.)
+            const float inv = __frcp_rn(s);
+            float y[8];
+            if (s >= 0x1p-80f) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 y = make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
-              codes[e >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
-                               << (16 * (e & 1));
+              for (int e = 0; e < 8; ++e) {
+                const float q = __fmul_rn(x[e], inv);
+                y[e] = __fmaf_rn(__fmaf_rn(-q, s, x[e]), inv, q);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], s);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              codes[e >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]),
+                                                                              __NV_SATFINITE, __NV_E4M3))
+                               << (16 * (e & 1));
           }
           *reinterpret_cast<uint2 *>(place.dst + c0) = make_uint2(codes[0], codes[1]);
           if (lane == 0) *scale_s[mine] = s_bits;
@@ -226,9 +262,11 @@ constexpr int kReadRows = 4;   // rows a thread has in flight
 constexpr int kReadLanes = 8;  // threads of a row
 constexpr int kReadAtOnce = kThreads / kReadLanes;
 
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-  const int which = blockIdx.y;
-  uint16_t *out = p.out[which];
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
+  const bool values = blockIdx.y != 0;
+  uint16_t *out = values ? p.out[1] : p.out[0];
+  const uint8_t *codes = values ? p.codes[1] : p.codes[0];
+  const uint16_t *scales = values ? p.scales[1] : p.scales[0];
   if (out == nullptr) return;
   const int rows_a_block = kReadAtOnce * kReadRows;
   const int chunks = (p.count + rows_a_block - 1) / rows_a_block;
@@ -246,8 +284,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
   for (int r = 0; r < kReadRows; ++r) {
     const int t = first + r * kReadAtOnce;
     if (t < rows) {
-      w[r] = __ldcs(reinterpret_cast<const uint4 *>(p.codes[which] + (in0 + t) * kByteRow) + lane);
-      s[r] = lo_f(p.scales[which][in0 + t]);
+      w[r] = __ldcs(reinterpret_cast<const uint4 *>(codes + (in0 + t) * kByteRow) + lane);
+      s[r] = lo_f(scales[in0 + t]);
     }
   }
 #pragma unroll
