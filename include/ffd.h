@@ -552,7 +552,11 @@ ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const 
  * first + j it sees, j < size.  A node that sees nothing yields a zero row;
  * what lies in unseen slots, NaN included, has no influence.  Rows i >= size
  * of out are left as they were.  Scores, softmax statistics and sums are fp32;
- * the softmax weights enter the product with V with 8 significant bits.
+ * the softmax weights enter the product with V with 8 significant bits.  Over an
+ * FFD_CACHE_BYTE cache so do the weights times V's scales, in units no coarser
+ * than 2^-16 of the largest one met so far, and the queries, in units no coarser
+ * than 2^-16 of the largest magnitude in the row (with at most 16 query rows a
+ * kv-head, num_nodes * Hq / Hkv: 2^-20 of the largest in any of them).
  * A sequence whose length is outside [0, cap], or whose size is outside [0,
  * min(num_nodes, length)], yields zero rows (all num_nodes) and sets
  * FFD_DEVICE_FLAG_BAD_LENGTH in the workspace (ffd_check_device_status).

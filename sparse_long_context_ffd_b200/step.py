@@ -16,7 +16,11 @@ to remove CPU launch overhead at small batch) applied to the FFD step:
   weights (there is no checkpoint): q, k and v projections of the hidden
   state, the FFD step, the output projection, captured whole.  The
   projections are plain library GEMMs (torch.matmul); every attention step
-  runs in the FFD kernel.
+  runs in the FFD kernel, with rotary positions before it where asked for.
+* :class:`TreeStep` -- verification of a tree of drafted tokens a sequence:
+  rotary positions and the cache write of all nodes (``ffd_append_tokens``),
+  their attention over the cache (``ffd_decode_tree``), captured whole, and the
+  accepted nodes' rows moved to where an accepted sequence has them.
 
 PyTorch provides the memory, streams and graphs; the compute of the attention
 step is the CUDA library's.
@@ -152,16 +156,18 @@ class StandInAttentionLayer:
     A step takes x [B, hidden] (pinned host ``host_x``), appends the new
     token's k/v to the caches, attends with FFD and writes the projected output
     [B, hidden] to ``host_y``.  lengths and ``advance`` as for DecodeStep (with
-    advance off every step re-appends at position lengths - 1).  No rotary
-    embedding or normalisation: this is a stand-in that exercises the step's
-    data flow, not a model.
+    advance off every step re-appends at position lengths - 1).  With `rope` (an
+    ffd.Rope) q and k are rotated in place by the new token's position, between
+    the projections and the step; the keys in the cache are then taken to be
+    rotated.  No normalisation: this is a stand-in that exercises the step's data
+    flow, not a model.
     """
 
     def __init__(self, shape: ffd.Shape, hidden: int, k_cache, v_cache, lengths, delta: float,
                  seed: int = 0, reference: int = ffd.FFD_REFERENCE_RUNNING_MAX, fmt: str = "int4",
-                 advance: bool = True):
+                 advance: bool = True, rope: Optional[ffd.Rope] = None):
         torch = _require_torch()
-        self.torch, self.shape = torch, shape
+        self.torch, self.shape, self.rope = torch, shape, rope
         dev = k_cache.device
         B, Hq, Hkv, D = shape.batch, shape.num_q_heads, shape.num_kv_heads, shape.head_dim
         gen = torch.Generator(device="cpu").manual_seed(int(seed))
@@ -178,6 +184,7 @@ class StandInAttentionLayer:
         self.host_y = torch.empty((B, hidden), dtype=torch.bfloat16).pin_memory()
         self._x = torch.empty((B, hidden), dtype=torch.bfloat16, device=dev)
         self._y = torch.empty((B, hidden), dtype=torch.bfloat16, device=dev)
+        self._position = torch.empty(B, dtype=torch.int32, device=dev)
         self._stream = torch.cuda.Stream(dev)
         self._graph = None
 
@@ -188,6 +195,9 @@ class StandInAttentionLayer:
         torch.matmul(self._x, self.w_q, out=c._q.view(B, -1))
         torch.matmul(self._x, self.w_k, out=c._k_new.view(B, -1))
         torch.matmul(self._x, self.w_v, out=c._v_new.view(B, -1))
+        if self.rope is not None:  # the new token's slot
+            torch.sub(c.lengths, 0 if c.advance else 1, out=self._position)
+            ffd.rotate(self.rope, self._position, c._q, c._q, c._k_new, c._k_new)
         c._launch()
         torch.matmul(c.bufs.out.view(B, -1), self.w_o, out=self._y)
         self.host_y.copy_(self._y, non_blocking=True)
@@ -212,3 +222,83 @@ class StandInAttentionLayer:
             self.capture()
         self._graph.replay()
         self.torch.cuda.current_stream(self._x.device).synchronize()
+
+
+class TreeStep:
+    """One attention layer's verification of drafted tokens, captured in a CUDA
+    graph.
+
+    cache: an ffd.KVCache of either format, whose first ``lengths`` tokens
+    (int32 [B], device) are the sequences so far.  A step takes up to num_nodes
+    drafted tokens a sequence from static device buffers that the caller fills:
+    ``q`` [B, n, Hq, 128], ``k_new``, ``v_new`` [B, n, Hkv, 128] (bf16, before
+    rotation), ``tree_mask`` int64 [B, n] and ``depth`` int32 [B, n]
+    (ffd.tree_from_parents makes both), ``sizes`` int32 [B].  They start as a
+    chain of num_nodes.  :meth:`step` rotates queries and keys by lengths + depth
+    (with `rope`), writes the nodes behind the sequences and attends; results are
+    in ``out`` [B, n, Hq, 128], on the current stream.  ``lengths`` stays: the
+    nodes are drafts until :meth:`accept` keeps some.  A sequence without room for
+    its nodes, or with more than num_nodes of them, yields zero rows and
+    FFD_DEVICE_FLAG_BAD_LENGTH (:meth:`check`).
+    """
+
+    def __init__(self, shape: ffd.Shape, cache: "ffd.KVCache", lengths, num_nodes: int,
+                 rope: Optional[ffd.Rope] = None):
+        torch = _require_torch()
+        self.torch, self.shape, self.cache, self.lengths, self.rope = torch, shape, cache, lengths, rope
+        B, Hq, Hkv, n = shape.batch, shape.num_q_heads, shape.num_kv_heads, int(num_nodes)
+        dev = lengths.device
+        bf16, i32 = torch.bfloat16, torch.int32
+        self.workspace = ffd.tree_workspace(shape, n, device=dev)
+        self.q, self.out, self._rotated = (torch.zeros((B, n, Hq, 128), dtype=bf16, device=dev) for _ in range(3))
+        self.k_new, self.v_new = (torch.zeros((B, n, Hkv, 128), dtype=bf16, device=dev) for _ in range(2))
+        mask, depth = ffd.tree_from_parents([list(range(-1, n - 1))] * B)
+        self.tree_mask, self.depth = mask.to(dev), depth.to(dev)
+        self.sizes = torch.full((B,), n, dtype=i32, device=dev)
+        self._total = torch.empty(B, dtype=i32, device=dev)
+        self._positions = torch.empty((B, n), dtype=i32, device=dev)
+        self._stream = torch.cuda.Stream(dev)
+        self._graph = None
+
+    def _body(self):
+        torch = self.torch
+        torch.add(self.lengths, self.sizes, out=self._total)
+        torch.add(self.lengths[:, None], self.depth, out=self._positions)
+        ffd.append_tokens(self.shape, self.cache, self.k_new, self.v_new, self._total, rope=self.rope,
+                          positions=self._positions, new_lengths=self.sizes, q=self.q, q_out=self._rotated)
+        ffd.decode_tree(self.shape, self.cache, self._rotated, self._total, self.out, self.workspace,
+                        tree_mask=self.tree_mask, tree_sizes=self.sizes)
+
+    def capture(self):
+        """Capture the step's graph (done by the first :meth:`step`).  Nothing
+        runs at capture."""
+        torch = self.torch
+        torch.cuda.synchronize(self.lengths.device)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=self._stream):
+            self._body()
+        self._graph = g
+        return g
+
+    def step(self):
+        """One verification step; returns ``out`` (not waited for)."""
+        if self._graph is None:
+            self.capture()
+        self._graph.replay()
+        return self.out
+
+    def accept(self, nodes, counts):
+        """Keep counts[b] nodes of each sequence, nodes[b, :counts[b]] in order
+        (int64 [B, m] and int32 [B], on the device; the rest of a row is
+        ignored): node i of the list becomes token lengths[b] + i, rotated for
+        that position, and ``lengths`` grows by counts.  The list is a path of the
+        tree from a root, so its keys are the ones already attended to."""
+        torch, B, m = self.torch, self.shape.batch, nodes.shape[1]
+        at = nodes.clamp(0, self.k_new.shape[1] - 1)[:, :, None, None].expand(B, m, self.shape.num_kv_heads, 128)
+        self.lengths.add_(counts)
+        ffd.append_tokens(self.shape, self.cache, self.k_new.gather(1, at), self.v_new.gather(1, at), self.lengths,
+                          rope=self.rope, new_lengths=counts)
+
+    def check(self) -> int:
+        """Device flags (ffd.FFD_DEVICE_FLAG_*) raised since the last check."""
+        return ffd.check_device_status(self.workspace)
