@@ -53,7 +53,7 @@ struct TreeParams {
   uint16_t *out;
   uint32_t *err;
   int2 *table;                  // [B][kv_heads][units a head]: first CTA * 2 + its slot, CTAs
-  float *partials;              // [ctas][2][rows][kPartialStride]
+  float *partials;              // [ctas][2][part_floats(rows)]
   int32_t batch, kv_heads, group_log2, nodes, capacity, format;
   int32_t units_a_head, rows, ctas;
 };

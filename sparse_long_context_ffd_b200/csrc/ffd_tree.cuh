@@ -106,6 +106,17 @@ struct Walk {
   }
 };
 
+// A part of a unit in the workspace: its rows' O, 32 channels after another as
+// [row][32], a row's eight 16-byte vectors in the order c ^ (row & 7) (as they
+// are staged in shared memory, free of bank conflicts), then (m, l) of the rows.
+__host__ __device__ constexpr size_t part_floats(int rows) { return (static_cast<size_t>(rows) * 130 + 3) / 4 * 4; }
+
+__device__ __forceinline__ size_t part_vector(int rows, int row, int vector) {  // of 32, four channels each
+  return (static_cast<size_t>(vector >> 3) * rows + row) * 32 + 4 * ((vector & 7) ^ (row & 7));
+}
+
+__device__ __forceinline__ size_t part_sums(int rows, int row) { return static_cast<size_t>(rows) * 128 + 2 * row; }
+
 // CTA c of the grid holds tiles part_begin(c) to part_begin(c + 1) of `total`;
 // of as many CTAs as there are tiles every one has one.
 __device__ __forceinline__ int part_begin(int total, int c) {
@@ -120,8 +131,18 @@ __device__ __forceinline__ int part_of(int total, int tile) {
 }
 
 // This CTA's part of the tiles: thread t adds up the sequences of its chunk.
-// start: the first sequence, the tile among its units', tiles, all tiles (CTA-wide
-// after the next __syncthreads).
+// start: the first sequence, the tile among its units', tiles, all tiles, and (or
+// 0) the CTAs of its unit (CTA-wide after the next __syncthreads).
+//
+// A CTA that goes on to a second unit ends the first and begins the next at a
+// cost of about four tiles (5 us; 64 nodes over 3 ragged contexts of up to 16K:
+// such CTAs took 65 us, the others 54).  So where there are no more than 32
+// sequences, and fewer units than CTAs, every unit is cut into equal pieces of
+// at most L tiles, one a CTA, with the smallest L for which there are CTAs
+// enough; unless L is more than kSegmentTiles above the equal share (4 x 8 units
+// of 256 tiles: 64 against 56).
+constexpr int kSegmentTiles = 4;
+
 template <int kThreads>
 __device__ __forceinline__ void find_part(const TreeParams &p, int *sum_s, int *start) {
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -158,16 +179,56 @@ __device__ __forceinline__ void find_part(const TreeParams &p, int *sum_s, int *
     start[1] = off;
     start[2] = end - begin;
   }
-  if (tid == 0) start[3] = total;
+  if (tid == 0) {
+    start[3] = total;
+    start[4] = 0;
+  }
+  if (warp == 0 && p.batch <= 32 && total > static_cast<int>(gridDim.x)) {
+    __syncwarp();
+    const int ctas = gridDim.x, t = sum / units;  // (chunk is 1)
+    if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, t > 0 ? units : 0)) <= ctas) {
+      const int share = (total + ctas - 1) / ctas;
+      int lo = share, hi = __reduce_max_sync(0xFFFFFFFFu, t);
+      if (hi < lo) hi = lo;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, units * ((t + mid - 1) / mid))) <= ctas) hi = mid;
+        else lo = mid + 1;
+      }
+      if (lo <= share + kSegmentTiles) {
+        const int pieces = (t + lo - 1) / lo, mine = units * pieces;
+        int to = mine;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int other = __shfl_up_sync(0xFFFFFFFFu, to, d);
+          if (tid >= d) to += other;
+        }
+        const int c = blockIdx.x, at = c - (to - mine), all = __shfl_sync(0xFFFFFFFFu, to, 31);
+        if (tid == 0) start[2] = 0;
+        __syncwarp();
+        if (at >= 0 && at < mine && c < all) {
+          const int unit = at / pieces, k = at - unit * pieces, each = t / pieces, longer = t - each * pieces;
+          start[0] = tid;
+          start[1] = unit * t + k * each + min(k, longer);
+          start[2] = each + (k < longer ? 1 : 0);
+          start[4] = pieces;
+        }
+      }
+    }
+  }
 }
 
 // Where merge_tree_kernel finds the parts of a unit whose first tile is here.
 __device__ __forceinline__ void note_unit(const TreeParams &p, const Segment &g, const Walk &walk, const int *start,
                                           bool starts) {
+  int2 *entry = p.table + static_cast<size_t>(g.b) * p.kv_heads * p.units_a_head + g.unit;
+  if (start[4] > 0) {
+    *entry = make_int2(2 * static_cast<int>(blockIdx.x), start[4]);
+    return;
+  }
   const int total = start[3];
   const int here = part_begin(total, blockIdx.x) + start[2] - walk.left - g.tiles;  // the unit's first tile
   const int c1 = part_of(total, here + g.all - 1);
-  p.table[static_cast<size_t>(g.b) * p.kv_heads * p.units_a_head + g.unit] =
+  *entry =
       make_int2(2 * static_cast<int>(blockIdx.x) + (starts ? 0 : 1), c1 - static_cast<int>(blockIdx.x) + 1);
 }
 

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     start_s[0] = start_s[1] = start_s[2] = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
+    if (!kByte) prefetch_tmap(&tmap_q);
   }
   find_part<kCtaThreads>(p, reinterpret_cast<int *>(row_s), start_s);
   tc_fence_before();
@@ -493,7 +494,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       }
       row_s[s * kGroup + t] = make_float2(m, l);
       tc_fence_after();
-      named_barrier(1, 2 * kGroup);
+      // (the other group's sums, or only what it found in the drafted tokens' rows)
+      if (!kPair || (g.tile0 + g.tiles) * kTile > first) named_barrier(1, 2 * kGroup);
+      else named_barrier(2 + s, kGroup);
       const bool whole = g.tiles == g.all;
       const bool any_odd = *odd != 0;
       float f0 = 1.0f, f1 = 0.0f, row_m = m, row_l = l;
@@ -515,13 +518,19 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         row_s[s * kGroup + t] = make_float2(row_m, row_l);  // every copy of the row the same
       }
       // 32 channels at a time through shared memory (the Q tile's, which no
-      // product reads any more): copies of a row are added, and a row's
-      // channels leave side by side
-      float4 *stage = reinterpret_cast<float4 *>(smem + (kPair ? s * kOutTile : s * (kOutTile / 2)));
-      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * p.rows * kPartialStride;
+      // product reads any more): copies of a row are added, and what is left goes
+      // out as one copy (a part), or row by row.
+      const int block_row = kPair ? s * kGroup : 0;   // of the unit
+      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * part_floats(p.rows);
+      const int rows_out = min(kRowsHere, p.rows - block_row);
+      if (!whole && (kPair || s == 0) && t < rows_out)
+        *reinterpret_cast<float2 *>(part_out + part_sums(p.rows, block_row + t)) = row_s[s * kGroup + t];
       constexpr int kChannels = kPair ? kHeadDim : kHeadDim / 2;
+#pragma unroll 1
       for (int c0 = 0; c0 < kChannels; c0 += 32) {
         const int ch = (kPair ? 0 : s * kChannels) + c0;
+        // (two stages where there is room for them)
+        float4 *stage = reinterpret_cast<float4 *>(smem + (kPair ? s * kOutTile + (c0 & 32) * 512 : s * (kOutTile / 2)));
         float o[32];
         if constexpr (kPair) {
           tmem_ld<32>(tm_o + ch, o);
@@ -539,45 +548,59 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
           }
         }
+        if (c0 >= (kPair ? 64 : 32)) {
+          if (t == 0) bulk_wait_read<kPair ? 1 : 0>();
+          named_barrier(2 + s, kGroup);
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           stage[t * 8 + (c ^ (t & 7))] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        if (any_odd && part == 0) {
+          float *mine = reinterpret_cast<float *>(stage + t * 8);
+#pragma unroll 1
+          for (int e = 0; e < 32; ++e)
+            mine[4 * ((e >> 2) ^ (t & 7)) + (e & 3)] += odd_values<kByte>(p, g, bh, seen, ch + e);
+        }
+        fence_proxy_async_smem();
         named_barrier(2 + s, kGroup);
+        if constexpr (kRep > 1) {
+#pragma unroll 1
+          for (int item = t; item < kRowsHere * 8; item += kGroup) {  // (row, place): every copy has the same place
+            float4 v = stage[item];
+#pragma unroll
+            for (int k = 1; k < kRep; ++k) {
+              const float4 u = stage[item + k * kRowsHere * 8];
+              v.x += u.x;
+              v.y += u.y;
+              v.z += u.z;
+              v.w += u.w;
+            }
+            stage[item] = v;
+          }
+          fence_proxy_async_smem();
+          named_barrier(2 + s, kGroup);
+        }
+        if (!whole) {
+          if (t == 0 && rows_out > 0) {
+            bulk_s2g(part_out + (static_cast<size_t>(ch >> 5) * p.rows + block_row) * 32, stage, rows_out * 128);
+            bulk_commit();
+          }
+          continue;
+        }
+#pragma unroll 1
         for (int item = t; item < kRowsHere * 8; item += kGroup) {
           const int r = item >> 3, c = item & 7, q_row = block + r, i = q_row >> p.group_log2;
-          if (i >= g.size) continue;
+          if (i >= g.size) break;
           float4 v = stage[r * 8 + (c ^ (r & 7))];
-#pragma unroll
-          for (int k = 1; k < kRep; ++k) {
-            const float4 u = stage[(r + k * kRowsHere) * 8 + (c ^ (r & 7))];
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
-          }
-          const int channel = ch + 4 * c;
-          if (any_odd) {
-            const uint64_t bits = seen_nodes(p, g, i);
-            float *y = &v.x;
-            for (int e = 0; e < 4; ++e) y[e] += odd_values<kByte>(p, g, bh, bits, channel + e);
-          }
-          const float2 ml = row_s[s * kGroup + r];
-          if (whole) {
-            const float inv = 1.0f / ml.y;
-            float *y = &v.x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = ml.y == 0.0f && y[e] == 0.0f ? 0.0f : y[e] * inv;
-            uint16_t *dst = p.out + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
-                            (q_row & ((1 << p.group_log2) - 1)) * kHeadDim + channel;
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-          } else {
-            float *dst = part_out + static_cast<size_t>((kPair ? s * kGroup : 0) + r) * kPartialStride;
-            *reinterpret_cast<float4 *>(dst + channel) = v;
-            if (channel == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = ml;
-          }
+          const float sum = row_s[s * kGroup + r].y, inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+          v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);  // (a row that saw nothing: 0)
+          uint16_t *dst = p.out + (((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) * kHeadDim +
+                          (q_row & ((1 << p.group_log2) - 1)) * kHeadDim + ch + 4 * c;
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
         named_barrier(2 + s, kGroup);
       }
+      if (t == 0) bulk_wait_read<0>();
       if (tid == 0 && g.tile0 == 0) note_unit(p, g, walk, start_s, starts);
       starts = false;
       tc_fence_before();
@@ -585,6 +608,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       named_barrier(1, 2 * kGroup);
       if (tid == 0) *odd = 0;
     }
+    if (t == 0) bulk_wait<0>();
   }
   __syncwarp();
   tc_fence_before();
@@ -621,11 +645,11 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   const int2 at = p.table[(static_cast<size_t>(b) * p.kv_heads + kv) * p.units_a_head + block];
   // (a part count beyond the grid can only be left over from a call that gave up)
   if (at.y <= 1 || at.x < 0 || (at.x >> 1) + at.y > p.ctas) return;
-  const float *base = p.partials + static_cast<size_t>(row - block * kTreeRows) * kPartialStride;
-  const size_t cta = static_cast<size_t>(2) * p.rows * kPartialStride;
+  const size_t slot = part_floats(p.rows);
   // part 0 is in the slot that the table names, the others begin their CTAs: slot 0
-  const float *part0 = base + static_cast<size_t>(at.x) * p.rows * kPartialStride;
-  const float *parts = base + static_cast<size_t>(at.x >> 1) * cta;
+  const int r0 = row - block * kTreeRows;
+  const size_t vector = part_vector(p.rows, r0, lane), sums = part_sums(p.rows, r0);
+  const float *part0 = p.partials + at.x * slot, *parts = p.partials + static_cast<size_t>(at.x >> 1) * 2 * slot;
   // four parts' loads in flight a warp, joined on a running maximum
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float l = 0.0f, m = -INFINITY;
@@ -638,9 +662,9 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
       ml[u] = make_float2(-INFINITY, 0.0f);
       o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (k < at.y) {
-        const float *from = k == 0 ? part0 : parts + k * cta;
-        ml[u] = *reinterpret_cast<const float2 *>(from + kHeadDim);
-        o[u] = reinterpret_cast<const float4 *>(from)[lane];
+        const float *from = k == 0 ? part0 : parts + 2 * k * slot;
+        ml[u] = *reinterpret_cast<const float2 *>(from + sums);
+        o[u] = *reinterpret_cast<const float4 *>(from + vector);
       }
     }
     const float next = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
@@ -761,7 +785,7 @@ TreeLayout tree_layout(int32_t batch, int32_t kv_heads, int32_t group, int32_t n
   L.ctas = static_cast<int32_t>(tiles < kTreeCtas ? tiles : kTreeCtas);
   L.table = 256;
   L.partials = L.table + (static_cast<size_t>(units) * 8 + 255) / 256 * 256;
-  L.total = (L.partials + static_cast<size_t>(L.ctas) * 2 * L.rows * kPartialStride * 4 + 255) / 256 * 256;
+  L.total = (L.partials + static_cast<size_t>(L.ctas) * 2 * part_floats(L.rows) * 4 + 255) / 256 * 256;
   return L;
 }
 

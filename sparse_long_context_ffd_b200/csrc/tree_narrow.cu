@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       named_barrier(bar_all, kGroups * kGroup);
       // four rows at a time, 32 channels a warp, one a lane
       constexpr int kMine = kRows / kGroups;
-      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * p.rows * kPartialStride;
+      float *part_out = p.partials + static_cast<size_t>(2 * blockIdx.x + (starts ? 0 : 1)) * part_floats(p.rows);
 #pragma unroll 1
       for (int r0 = s * kMine; r0 < (s + 1) * kMine && (r0 >> p.group_log2) < g.size; r0 += 4) {
         float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -513,9 +513,8 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
               p.out[((((static_cast<size_t>(g.b) * p.nodes + i) * p.kv_heads + head) << p.group_log2) +
                      (r & ((1 << p.group_log2) - 1))) * kHeadDim + t] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
             } else {
-              float *dst = part_out + static_cast<size_t>(r) * kPartialStride;
-              dst[t] = o[e];
-              if (t == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = tot_s[r];
+              part_out[part_vector(p.rows, r, t >> 2) + (t & 3)] = o[e];
+              if (t == 0) *reinterpret_cast<float2 *>(part_out + part_sums(p.rows, r)) = tot_s[r];
             }
           }
         }
