@@ -22,6 +22,58 @@ __device__ __forceinline__ float exp2_f(float x) {
   return y;
 }
 
+// Two fp32 values in one 64-bit register: one instruction does both.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void one_each(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 2^z of two values on the multiply-add pipe, for a part of a tile's weights:
+// the exponential unit gives 16 a clock and multiprocessor, and would set the
+// pace alone.  z is taken apart into the nearest whole number n (adding 1.5 2^23
+// rounds to it) and f in [-0.5, 0.5]; 2^f is a polynomial of degree 4, of least
+// relative error 2.6e-6 (found by Remez's exchange; a weight is rounded to 2^-9);
+// 2^n is made of its bits.  z up to 127; below -126 it gives 2^-126, and NaN
+// stays NaN.
+__device__ __forceinline__ void exp2_poly2(uint64_t z, float &a, float &b) {
+  float z0, z1;
+  one_each(z, z0, z1);
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(z0));  // -126
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(z1));
+  z = two(z0, z1);
+  constexpr float kRound = 12582912.0f;
+  const uint64_t n = add2(z, two(kRound, kRound));
+  const uint64_t f = fma2(add2(n, two(-kRound, -kRound)), two(-1.0f, -1.0f), z);
+  uint64_t y = fma2(f, two(0.009570102207362652f, 0.009570102207362652f), two(0.05591785907745361f, 0.05591785907745361f));
+  y = fma2(y, f, two(0.240247443318367f, 0.240247443318367f));
+  y = fma2(y, f, two(0.6931217908859253f, 0.6931217908859253f));
+  y = fma2(y, f, two(0.9999992847442627f, 0.9999992847442627f));
+  float n0, n1;
+  one_each(n, n0, n1);
+  y = mul2(y, two(__uint_as_float((__float_as_uint(n0) << 23) + 0x3F800000u),
+                  __uint_as_float((__float_as_uint(n1) << 23) + 0x3F800000u)));
+  one_each(y, a, b);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);

@@ -122,10 +122,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     return alive;
   };
 
-  // Registers move from the last four warps to the softmax groups: 2 x 128 x
-  // 208 + 128 x 88 are the 384 x 168 that the CTA starts with.
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
     // ------------------------------------------------------------- copies --
     // (the whole warp walks and waits, one lane issues)
@@ -236,7 +233,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int s = warp >> 2;                     // group
     const int t = tid & (kGroup - 1);            // lane of the accumulator
     const int w = warp & 3;
@@ -349,129 +345,159 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         ++s_count;
         tc_fence_after();
         if ((kPair ? s == 1 : true) && t == 0) mbar_arrive(empty + (vi - 1) % kSlots);  // K is read
-        float x[kCols];
+        // 64 tokens at a time; of 128 the first 64 stay in registers for their
+        // weights, the others are read twice.  (All 128 do not fit beside the
+        // rest, and what a thread spills passes through the memory that feeds the
+        // matrix instructions: with 180 bytes of it a tile took half as long again.)
+        constexpr int kPart = kCols < 64 ? kCols : 64;
+        auto load = [&](int c0, float (&x)[kPart]) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld<32>(tm_s + part * kCols + c, x + c);
-        tmem_wait_ld<32>(x);
+          for (int c = 0; c < kPart; c += 32) tmem_ld<32>(tm_s + part * kCols + c0 + c, x + c);
+          tmem_wait_ld<32>(x);
 #pragma unroll
-        for (int c = 32; c < kCols; c += 32) tmem_wait_ld<32, false>(x + c);
-        if constexpr (kByte) {
+          for (int c = 32; c < kPart; c += 32) tmem_wait_ld<32, false>(x + c);
+          if constexpr (kByte) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 ks = tok[c >> 2];
-            x[c] *= ks.x;
-            x[c + 1] *= ks.y;
-            x[c + 2] *= ks.z;
-            x[c + 3] *= ks.w;
+            for (int c = 0; c < kPart; c += 4) {
+              const float4 ks = tok[(c0 + c) >> 2];
+              x[c] *= ks.x;
+              x[c + 1] *= ks.y;
+              x[c + 2] *= ks.z;
+              x[c + 3] *= ks.w;
+            }
           }
-        }
-        if (masked) {
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            const int at = t0 + part * kCols + c - first;  // the first column's node (below 0: before the tree)
-            uint32_t bits;
-            if (at <= -32)
-              bits = ~0u;
-            else if (at < 0)
-              bits = static_cast<uint32_t>(seen << -at) | ((1u << -at) - 1u);
-            else
-              bits = at < 64 ? static_cast<uint32_t>(seen >> at) : 0u;
+            for (int c = 0; c < kPart; c += 32) {
+              const int at = t0 + part * kCols + c0 + c - first;  // the first column's node (below 0: before the tree)
+              uint32_t bits;
+              if (at <= -32)
+                bits = ~0u;
+              else if (at < 0)
+                bits = static_cast<uint32_t>(seen << -at) | ((1u << -at) - 1u);
+              else
+                bits = at < 64 ? static_cast<uint32_t>(seen >> at) : 0u;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((bits >> e) & 1u)) x[c + e] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[c + e] = -INFINITY;
+            }
           }
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (kByte) {
+        };
+        auto highest = [&](int c0, const float (&x)[kPart]) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if constexpr (kByte) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 lv = tok[(2 * kTile + c) >> 2];
-            top[0] = fmaxf(top[0], fmaf(x[c], score_scale, lv.x));
-            top[1] = fmaxf(top[1], fmaf(x[c + 1], score_scale, lv.y));
-            top[2] = fmaxf(top[2], fmaf(x[c + 2], score_scale, lv.z));
-            top[3] = fmaxf(top[3], fmaf(x[c + 3], score_scale, lv.w));
+            for (int c = 0; c < kPart; c += 4) {
+              const float4 lv = tok[(2 * kTile + c0 + c) >> 2];
+              top[0] = fmaxf(top[0], fmaf(x[c], score_scale, lv.x));
+              top[1] = fmaxf(top[1], fmaf(x[c + 1], score_scale, lv.y));
+              top[2] = fmaxf(top[2], fmaf(x[c + 2], score_scale, lv.z));
+              top[3] = fmaxf(top[3], fmaf(x[c + 3], score_scale, lv.w));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kPart; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        };
+        float x[kPart], high = -INFINITY;
+        if constexpr (kCols > kPart) {
+          load(kPart, x);
+          high = highest(kPart, x);
         }
-        float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        load(0, x);
+        high = fmaxf(high, highest(0, x));
         // The reference m moves only when weights would leave their range: in
         // bf16 past 2^8; in e4m3 past 448 (2^8.8), from 2^7 at the last move,
         // so that small weights keep their bits.  O follows, which is idle:
         // the product before the one that made S was the last to add to it.
-        constexpr float kRoom = kByte ? 8.8f : 8.0f;
+        constexpr float kRoom = kByte ? 8.8f - 7.0f : 8.0f;
         if constexpr (kByte) high -= 7.0f; else high *= kScoreScale;
         if (j < 2 && (kPair ? j == 0 : true)) {
           m = high;
-        } else if (__any_sync(0xFFFFFFFFu, high > m + (kByte ? kRoom - 7.0f : kRoom))) {
+        } else if (__any_sync(0xFFFFFFFFu, high > m + kRoom)) {
           const float next = fmaxf(m, high);
           const float f = next == m ? 1.0f : exp2_f(m - next);
           m = next;
           l *= f;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 16) {
+            float o[16];
+            tmem_ld<16>(tm_o + c, o);
+            tmem_wait_ld<16>(o);
 #pragma unroll
-          for (int c = 0; c < kHeadDim; c += 32) {
-            float o[32];
-            tmem_ld<32>(tm_o + c, o);
-            tmem_wait_ld<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st<32>(tm_o + c, reinterpret_cast<const uint32_t *>(o));
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tmem_st<16>(tm_o + c, reinterpret_cast<const uint32_t *>(o));
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (kByte) {
-          uint32_t hi[kCols / 4], lo[kCols / 4];
+        const uint64_t scale2 = two(score_scale, score_scale), ref2 = two(-ref, -ref);
+        uint64_t sums[2] = {0, 0};
+        // Weights of 64 tokens, into columns of S that have been read.  Of every
+        // eight pairs three by polynomial, but not where there are masked ones:
+        // their weight has to be 0, which the polynomial does not give.
+        auto weigh = [&](int c0, const float (&x)[kPart], bool plain) {
+          uint32_t w[kPart / 2];  // bf16 pairs; e4m3: first parts, then second
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 vs = tok[(kTile + c) >> 2];
-            const float p0 = exp2_f(fmaf(x[c], score_scale, -ref)), p1 = exp2_f(fmaf(x[c + 1], score_scale, -ref));
-            const float p2 = exp2_f(fmaf(x[c + 2], score_scale, -ref)), p3 = exp2_f(fmaf(x[c + 3], score_scale, -ref));
-            sum[0] += p0;
-            sum[1] += p1;
-            sum[2] += p2;
-            sum[3] += p3;
-            split4(p0 * vs.x, p1 * vs.y, p2 * vs.z, p3 * vs.w, hi[c >> 2], lo[c >> 2]);
+          for (int c = 0; c < kPart; c += 4) {
+            float q[4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const uint64_t z = fma2(two(x[c + e], x[c + e + 1]), scale2, ref2);
+              constexpr uint32_t kPoly = kByte ? 0u : 0x52u;
+              if (!plain && ((kPoly >> (((c + e) >> 1) & 7)) & 1u)) {
+                exp2_poly2(z, q[e], q[e + 1]);
+              } else {
+                one_each(z, q[e], q[e + 1]);
+                q[e] = exp2_f(q[e]);
+                q[e + 1] = exp2_f(q[e + 1]);
+              }
+              sums[e >> 1] = add2(sums[e >> 1], two(q[e], q[e + 1]));
+            }
+            if constexpr (kByte) {
+              const float4 vs = tok[(kTile + c0 + c) >> 2];
+              split4(q[0] * vs.x, q[1] * vs.y, q[2] * vs.z, q[3] * vs.w, w[c >> 2], w[kPart / 4 + (c >> 2)]);
+            } else {
+              w[c >> 1] = pack_bf16(q[0], q[1]);
+              w[(c >> 1) + 1] = pack_bf16(q[2], q[3]);
+            }
           }
-          constexpr int kWide = kCols / 4;
+          if constexpr (kByte) {
+            tmem_st<kPart / 4>(tm_s + (part * kCols + c0) / 4, w);
+            tmem_st<kPart / 4>(tm_s + 32 + (part * kCols + c0) / 4, w + kPart / 4);
+          } else {
+            tmem_st<kPart / 2>(tm_s + (part * kCols + c0) / 2, w);
+          }
+        };
+        if (kByte || masked) {
+          weigh(0, x, true);
+          if constexpr (kCols > kPart) {
+            load(kPart, x);
+            weigh(kPart, x, true);
+          }
+        } else {
+          weigh(0, x, false);
+          if constexpr (kCols > kPart) {
+            load(kPart, x);
+            weigh(kPart, x, false);
+          }
+        }
+        if constexpr (kRep > 1) {
+          // a copy of the row has no weights for the other copies' tokens
+          constexpr int kWide = kByte ? kCols / 4 : kCols / 2;
           uint32_t none[kWide];
 #pragma unroll
           for (int c = 0; c < kWide; ++c) none[c] = 0u;
 #pragma unroll
-          for (int r = 0; r < kRep; ++r) {
-            if (r == part) {
-              tmem_st<kWide>(tm_s + r * kWide, hi);
-              tmem_st<kWide>(tm_s + 32 + r * kWide, lo);
-            } else {
-              tmem_st<kWide>(tm_s + r * kWide, none);
-              tmem_st<kWide>(tm_s + 32 + r * kWide, none);
-            }
-          }
-        } else {
-          uint32_t pairs[kCols / 2];
-#pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            const float p0 = exp2_f(fmaf(x[c], kScoreScale, -ref)), p1 = exp2_f(fmaf(x[c + 1], kScoreScale, -ref));
-            sum[c & 2] += p0;
-            sum[(c & 2) + 1] += p1;
-            pairs[c >> 1] = pack_bf16(p0, p1);
-          }
-          if constexpr (kRep == 1) {
-            tmem_st<32>(tm_s, pairs);
-            tmem_st<32>(tm_s + 32, pairs + 32);
-          } else {
-            constexpr int kWide = kCols / 2;
-            uint32_t none[kWide];
-#pragma unroll
-            for (int c = 0; c < kWide; ++c) none[c] = 0u;
-#pragma unroll
-            for (int r = 0; r < kRep; ++r) {
-              if (r == part) tmem_st<kWide>(tm_s + r * kWide, pairs);
-              else tmem_st<kWide>(tm_s + r * kWide, none);
-            }
+          for (int r = 1; r < kRep; ++r) {
+            const int at = ((part + r) & (kRep - 1)) * kWide;
+            tmem_st<kWide>(tm_s + at, none);
+            if constexpr (kByte) tmem_st<kWide>(tm_s + 32 + at, none);
           }
         }
+        float sum[4];
+        one_each(sums[0], sum[0], sum[1]);
+        one_each(sums[1], sum[2], sum[3]);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         if (masked) {
