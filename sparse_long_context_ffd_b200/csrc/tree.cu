@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     // weights it is written, has gone out (products of a thread run in the order
     // of their issue), O += when V and the weights are there, whichever is first.
     // A commit holds the thread until what the last one stands for is done, and
-    // until the next issue the tensor cores stand still: so one commit a product
-    // where it can be, and lanes that ask the barriers at once.
+    // until the next issue the tensor cores stand still: so the commits come last,
+    // and lanes ask the barriers at once.
     uint32_t n = 0, segments = 0, p_phases = 0;
     // (lane 0's copy: known to be the same in every lane, such values stay in
     // uniform registers)
@@ -198,30 +198,32 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         }
         spin = 0;
         tc_fence_after();
-        if (do_o) {
-          const uint32_t add = uniform(oi < 2 ? 0 : 1), v = ring + v_slot * L::kSlot, tm = tm0 + 128 * og;
-          if (elect_one()) {
+        const uint32_t add = uniform(oi < 2 ? 0 : 1), v = ring + v_slot * L::kSlot, tm_v = tm0 + 128 * og;
+        const uint32_t k = ring + k_slot * L::kSlot, q = q0 + (kPair ? sg * kOutTile : 0), tm_k = tm0 + 128 * sg;
+        if (elect_one()) {
+          if (do_o) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)  // bf16: 16 tokens a step; e4m3: 32, first parts, then second
-              mma_ts<kByte>(tm + 256, tm + 8 * c, smem_desc(v + (kByte ? (c & 3) * 4096 : c * 2048), 16384), kIdescO,
+              mma_ts<kByte>(tm_v + 256, tm_v + 8 * c, smem_desc(v + (kByte ? (c & 3) * 4096 : c * 2048), 16384), kIdescO,
                             c > 0 || add != 0);
-            if (!kPair || og == 1) mma_commit(empty + v_slot);
-            if (oi >= items - 2) mma_commit(bar_o + og);
           }
-          p_phases ^= 1u << og;
-          ++oi;
-        }
-        if (do_s) {
-          const uint32_t k = ring + k_slot * L::kSlot, q = q0 + (kPair ? sg * kOutTile : 0), tm = tm0 + 128 * sg;
-          if (elect_one()) {
+          if (do_s) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)  // bf16: 16 channels a step, four a 128-byte half; e4m3: 32, Q's first part, then its second
-              mma_ss<kByte>(tm, smem_desc(q + (c >> 2) * 16384 + (c & 3) * 32),
+              mma_ss<kByte>(tm_k, smem_desc(q + (c >> 2) * 16384 + (c & 3) * 32),
                             smem_desc(k + (kByte ? 0 : (c >> 2) * 16384) + (c & 3) * 32), kIdescS, c > 0);
             mma_commit(bar_s + sg);
           }
-          ++si;
+          if (do_o) {
+            if (!kPair || og == 1) mma_commit(empty + v_slot);
+            if (oi >= items - 2) mma_commit(bar_o + og);
+          }
         }
+        if (do_o) {
+          p_phases ^= 1u << og;
+          ++oi;
+        }
+        if (do_s) ++si;
         __syncwarp();
       }
       n += g.tiles;

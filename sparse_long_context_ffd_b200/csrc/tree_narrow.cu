@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     // is there and the group has read its last S, O += of one when V and the
     // weights are there, whichever is first: neither holds up the other's slot.
     // A commit holds the thread until what the last one stands for is done, and
-    // until the next issue the tensor cores stand still: so one commit a product,
+    // until the next issue the tensor cores stand still: so the commits come last,
     // and four lanes ask the four barriers at once.
     uint32_t n = 0, segments = 0, p_phases = 0, f_phases = (1u << kGroups) - 1u;
     // (lane 0's copy: known to be the same in every lane, such values stay in
@@ -209,28 +209,29 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
         }
         spin = 0;
         tc_fence_after();
-        if (do_o) {
-          const uint32_t add = uniform(oi < kGroups ? 0 : 1), v = ring + v_slot * L::kSlot;
-          const uint32_t d = tm + (kGroups + og) * kN, w = q + L::kWeights + og * 128 * kRowBytes;
-          if (elect_one()) {
+        const uint32_t add = uniform(oi < kGroups ? 0 : 1), v = ring + v_slot * L::kSlot, k = ring + k_slot * L::kSlot;
+        const uint32_t o = tm + (kGroups + og) * kN, w = q + L::kWeights + og * 128 * kRowBytes, d = tm + sg * kN;
+        if (elect_one()) {
+          if (do_o) {
 #pragma unroll
             for (int c = 0; c < kSteps; ++c)  // bf16: 16 tokens a step; e4m3: 32
-              mma_ss<kByte>(d, smem_desc(v + c * (kByte ? 4096 : 2048), 16384),
+              mma_ss<kByte>(o, smem_desc(v + c * (kByte ? 4096 : 2048), 16384),
                             smem_desc<kRowBytes>(w + c * (kByte ? 32 : 16) * kRowBytes), kIdescO, c > 0 || add != 0);
-            mma_commit(empty + v_slot);
           }
-          p_phases ^= 1u << og;
-          ++oi;
-        }
-        if (do_s) {
-          const uint32_t k = ring + k_slot * L::kSlot, d = tm + sg * kN;
-          if (elect_one()) {
+          if (do_s) {
 #pragma unroll
             for (int c = 0; c < kSteps; ++c)  // bf16: 16 channels a step, four a 128-byte half; e4m3: 32
               mma_ss<kByte>(d, smem_desc(k + (c >> 2) * 16384 + (c & 3) * 32),
                             smem_desc(q + (c >> 2) * kN * 128 + (c & 3) * 32), kIdescS, c > 0);
             mma_commit(bar_s + sg);
           }
+          if (do_o) mma_commit(empty + v_slot);
+        }
+        if (do_o) {
+          p_phases ^= 1u << og;
+          ++oi;
+        }
+        if (do_s) {
           f_phases ^= 1u << sg;
           ++si;
         }
