@@ -198,6 +198,7 @@ constexpr int kSegmentTiles = 4;
 template <int kThreads>
 __device__ __forceinline__ void find_part(const TreeParams &p, int *sum_s, int *start) {
   const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) start[0] = start[1] = start[2] = start[4] = 0;
   const int chunk = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, tid * chunk), b1 = min(p.batch, b0 + chunk);
   const int units = p.kv_heads * p.units_a_head;
@@ -231,21 +232,17 @@ __device__ __forceinline__ void find_part(const TreeParams &p, int *sum_s, int *
     start[1] = off;
     start[2] = end - begin;
   }
-  if (tid == 0) {
-    start[3] = total;
-    start[4] = 0;
-  }
+  if (tid == 0) start[3] = total;
   if (warp == 0 && p.batch <= 32 && total > static_cast<int>(gridDim.x)) {
     __syncwarp();
     const int ctas = gridDim.x, t = sum / units;  // (chunk is 1)
     if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, t > 0 ? units : 0)) <= ctas) {
       const int share = (total + ctas - 1) / ctas;
-      int lo = share, hi = __reduce_max_sync(0xFFFFFFFFu, t);
-      if (hi < lo) hi = lo;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, units * ((t + mid - 1) / mid))) <= ctas) hi = mid;
-        else lo = mid + 1;
+      int lo = share + kSegmentTiles + 1;
+#pragma unroll
+      for (int more = kSegmentTiles; more >= 0; --more) {
+        const int pieces = units * ((t + share + more - 1) / (share + more));
+        if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, pieces)) <= ctas) lo = share + more;
       }
       if (lo <= share + kSegmentTiles) {
         const int pieces = (t + lo - 1) / lo, mine = units * pieces;

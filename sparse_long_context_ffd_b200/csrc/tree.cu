@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
-  if (tid == 0) {
+  if (tid == 8 * 32) {  // (warp 0 divides the work meanwhile)
     for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_s + s, 1);
@@ -94,7 +94,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     fence_mbar_init();
     *dead = 0;
     *odd = 0;
-    start_s[0] = start_s[1] = start_s[2] = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
     if (!kByte) prefetch_tmap(&tmap_q);
@@ -122,6 +121,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     return alive;
   };
 
+  // bf16: the query rows.  Rows past the tree are whatever lies there: no other
+  // row's result has anything of them.
+  auto load_query = [&](const Segment &g) {
+    constexpr int kTiles = kPair ? 2 : 1;
+    const int head = g.unit / p.units_a_head, row0 = (g.unit - head * p.units_a_head) * kTreeRows;
+    mbar_arrive_expect_tx(bar_q, kTiles * kOutTile);
+#pragma unroll
+    for (int i = 0; i < 2 * kTiles * kRep; ++i) {
+      const int q_tile = i / (2 * kRep), half = i & 1, copy = (i >> 1) % kRep;
+      tma_load_4d(smem + q_tile * kOutTile + half * 16384 + copy * kRowsHere * 128, &tmap_q, half * 64, 0, head,
+                  g.b * p.nodes + ((row0 + q_tile * kGroup) >> p.group_log2), bar_q);
+    }
+  };
+
   if (warp >= 8) {
     if (warp == 8) {
     // ------------------------------------------------------------- copies --
@@ -129,6 +142,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     {
       uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
       while (alive && walk.next(p, g)) {
+        if (!kByte && i == 0 && elect_one()) load_query(g);
+        __syncwarp();
         const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
         for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
           const uint32_t slot = i % kSlots, round = i / kSlots;
@@ -302,16 +317,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar_q);
-      } else if (tid == 0) {
-        // rows past the tree are whatever lies there: no other row's result has anything of them
-        constexpr int kTiles = kPair ? 2 : 1;
-        mbar_arrive_expect_tx(bar_q, kTiles * kOutTile);
-#pragma unroll
-        for (int i = 0; i < 2 * kTiles * kRep; ++i) {
-          const int q_tile = i / (2 * kRep), half = i & 1, copy = (i >> 1) % kRep;
-          tma_load_4d(smem + q_tile * kOutTile + half * 16384 + copy * kRowsHere * 128, &tmap_q, half * 64, 0, head,
-                      g.b * p.nodes + ((block + q_tile * kGroup) >> p.group_log2), bar_q);
-        }
+      } else if (tid == 0 && !starts) {  // (the first segment's: the copy warp, before K and V)
+        load_query(g);
       }
 
       // ---- the tiles ----
@@ -660,8 +667,8 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   const int b = bi / p.nodes, i = bi - b * p.nodes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t *out = p.out + static_cast<size_t>(blockIdx.x) * kHeadDim;
+  const Sequence q(p, b);  // (an input, not something the kernel before leaves)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Sequence q(p, b);
   if (!q.good) {
     if (threadIdx.x == 0 && i == 0 && head == 0) atomicOr(p.err, kFlagBadLength);
     out[threadIdx.x] = 0;

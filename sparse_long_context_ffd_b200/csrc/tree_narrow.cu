@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == kMatrixWarp) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), L::kTmem);
-  if (tid == 0) {
+  if (tid == kCopyWarp * 32) {  // (warp 0 divides the work meanwhile)
     for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
     for (int s = 0; s < kGroups; ++s) {
       mbar_init(bar_s + s, 1);
@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     fence_mbar_init();
     *dead = 0;
     *odd = 0;
-    start_s[0] = start_s[1] = start_s[2] = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
