@@ -560,9 +560,9 @@ ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const 
  * A sequence whose length is outside [0, cap], or whose size is outside [0,
  * min(num_nodes, length)], yields zero rows (all num_nodes) and sets
  * FFD_DEVICE_FLAG_BAD_LENGTH in the workspace (ffd_check_device_status).
- * 1 <= num_nodes <= FFD_MAX_TREE_NODES.  The result does not depend on what
- * the workspace held.  Calls that share a workspace must not overlap on the
- * GPU. */
+ * 1 <= num_nodes <= FFD_MAX_TREE_NODES, B * num_nodes * Hq < 2^31.  The result
+ * does not depend on what the workspace held.  Calls that share a workspace
+ * must not overlap on the GPU. */
 ffd_status ffd_decode_tree(const ffd_shape *shape, const ffd_cache *cache, int32_t num_nodes,
                            const void *q_bf16, const int32_t *d_lengths,
                            const int32_t *d_tree_sizes, const uint64_t *d_tree_mask,

@@ -52,8 +52,8 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
 // The angles come first: thread t finds (cos, sin) of one pair of one token
 // and leaves them in shared memory, since every head of the token needs them.
 // position * turns wraps at whole turns in 64 bits; its top 32 bits, signed,
-// are the angle in turns to 2^-32, and sincospif takes it from there.  Thread t
-// also finds where row t comes from and goes to, once instead of 16 times.
+// are the angle in turns to 2^-32, and sincospif takes it from there.  Where a
+// row comes from and goes to is found by one thread instead of 16.
 //
 // Then 16 threads take rows of one token, kInFlight before the first is used (a
 // block has 16 KB on its way from HBM), each with the angles of its channels in
@@ -71,7 +71,7 @@ struct RowPlace {
 };
 
 template <bool kAppend, bool kByte>
-__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant__ RowsParams p, int tokens_a_block,
+__global__ void __launch_bounds__(kThreads, kByte ? 4 : 5) rows_kernel(const __grid_constant__ RowsParams p, int tokens_a_block,
                                                         int rows_a_block) {
   extern __shared__ float2 turn_s[];  // [tokens_a_block][half]
   __shared__ RowPlace place_s[kTableRows];
@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
   const int row_begin = blockIdx.y * rows_a_block;
   const int width = min(rows, row_begin + rows_a_block) - row_begin;
   const int todo = tokens_here * width;
-  if (static_cast<int>(threadIdx.x) < todo) {
-    const int tl = threadIdx.x / width, row = row_begin + threadIdx.x - tl * width;
+  for (int r = threadIdx.x; r < todo; r += kThreads) {
+    const int tl = r / width, row = row_begin + r - tl * width;
     const int token = token0 + tl;
     const int kind = row < q_rows ? 0 : row < q_rows + kv_rows ? 1 : 2;
     const int head = kind == 0 ? row : (row - q_rows) - (kind == 2 ? kv_rows : 0);
@@ -104,13 +104,13 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
     } else if (kAppend) {
       const size_t to = (static_cast<size_t>(b) * p.kv_heads + head) * p.capacity + slot;
       at.dst = static_cast<uint8_t *>(kind == 1 ? p.k_out : p.v_out) + to * (kByte ? kByteRow : 2 * kHeadDim);
-      if (kByte) scale_s[threadIdx.x] = (kind == 1 ? p.k_scales : p.v_scales) + to;
+      if (kByte) scale_s[r] = (kind == 1 ? p.k_scales : p.v_scales) + to;
     } else {
       at.dst = static_cast<uint8_t *>(p.k_out) + (static_cast<size_t>(token) * kv_rows + head) * (2 * kHeadDim);
     }
     if (slot < 0) at.dst = nullptr;
-    place_s[threadIdx.x] = at;
-    kind_s[threadIdx.x] = static_cast<uint8_t>(kind);
+    place_s[r] = at;
+    kind_s[r] = static_cast<uint8_t>(kind);
   }
   for (int t = threadIdx.x; t < tokens_here * half; t += kThreads) {
     const int tl = t / half, token = token0 + tl;
@@ -256,9 +256,11 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
   }
 }
 
-// Sixteen codes (16 bytes in, 32 out) a thread and row; code * scale is exact in
-// fp32 (4 and 8 significant bits), so the only rounding is the one to bf16.
-constexpr int kReadRows = 4;   // rows a thread has in flight
+// Sixteen codes (16 bytes in, 32 out) a thread; code * scale is exact in fp32 (4
+// and 8 significant bits), so the only rounding is the one to bf16.  Bound by HBM
+// (4 x 8 x 32768 tokens: 140 us, 5.8 TB/s; 18 MB: 7.2 us).  One row a thread and
+// more blocks beat several rows in flight a thread: 2, 4 and 8 of them took 141,
+// 144 and 154 us, and 8.1, 8.2 and 9.0 us of the 18 MB.
 constexpr int kReadLanes = 8;  // threads of a row
 constexpr int kReadAtOnce = kThreads / kReadLanes;
 
@@ -268,43 +270,30 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   const uint8_t *codes = values ? p.codes[1] : p.codes[0];
   const uint16_t *scales = values ? p.scales[1] : p.scales[0];
   if (out == nullptr) return;
-  const int rows_a_block = kReadAtOnce * kReadRows;
-  const int chunks = (p.count + rows_a_block - 1) / rows_a_block;
+  const int chunks = (p.count + kReadAtOnce - 1) / kReadAtOnce;
   const int bh = blockIdx.x / chunks;
   const int len = p.lengths[bh / p.kv_heads];
   if (len < 0 || len > p.capacity) return;
   const int rows = min(p.count, len - p.begin);
   const int lane = threadIdx.x & (kReadLanes - 1);
-  const int first = (blockIdx.x - bh * chunks) * rows_a_block + threadIdx.x / kReadLanes;
+  const int t = (blockIdx.x - bh * chunks) * kReadAtOnce + threadIdx.x / kReadLanes;
+  if (t >= rows) return;
   const size_t in0 = static_cast<size_t>(bh) * p.capacity + p.begin;
   const size_t out0 = static_cast<size_t>(bh) * p.count;
-  uint4 w[kReadRows];
-  float s[kReadRows];
+  const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(codes + (in0 + t) * kByteRow) + lane);
+  const float s = lo_f(scales[in0 + t]);
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  uint32_t y[8];
 #pragma unroll
-  for (int r = 0; r < kReadRows; ++r) {
-    const int t = first + r * kReadAtOnce;
-    if (t < rows) {
-      w[r] = __ldcs(reinterpret_cast<const uint4 *>(codes + (in0 + t) * kByteRow) + lane);
-      s[r] = lo_f(scales[in0 + t]);
-    }
+  for (int e = 0; e < 8; ++e) {
+    const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>(words[e >> 1] >> (16 * (e & 1)));
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    y[e] = pack_bf16(f.x * s, f.y * s);
   }
-#pragma unroll
-  for (int r = 0; r < kReadRows; ++r) {
-    const int t = first + r * kReadAtOnce;
-    if (t >= rows) continue;
-    const uint32_t words[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-    uint32_t y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>(words[e >> 1] >> (16 * (e & 1)));
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-      y[e] = pack_bf16(f.x * s[r], f.y * s[r]);
-    }
-    uint4 *dst = reinterpret_cast<uint4 *>(out + (out0 + t) * kHeadDim) + 2 * lane;
-    __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
-    __stcs(dst + 1, make_uint4(y[4], y[5], y[6], y[7]));
-  }
+  uint4 *dst = reinterpret_cast<uint4 *>(out + (out0 + t) * kHeadDim) + 2 * lane;
+  __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
+  __stcs(dst + 1, make_uint4(y[4], y[5], y[6], y[7]));
 }
 
 template <bool kAppend, bool kByte>
@@ -332,8 +321,7 @@ cudaError_t launch_rows(const RowsParams &p, bool append, int format, cudaStream
 }
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream) {
-  const int rows = kReadAtOnce * kReadRows;
-  const dim3 grid(static_cast<unsigned>((p.count + rows - 1) / rows) * static_cast<unsigned>(p.batch * p.kv_heads), 2);
+  const dim3 grid(static_cast<unsigned>((p.count + kReadAtOnce - 1) / kReadAtOnce) * static_cast<unsigned>(p.batch * p.kv_heads), 2);
   read_kernel<<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -258,6 +258,8 @@ ffd_status ffd_decode_tree(const ffd_shape *s, const ffd_cache *c, int32_t num_n
   if (st != FFD_OK) return st;
   if (num_nodes < 1 || num_nodes > FFD_MAX_TREE_NODES) return FFD_ERR_INVALID_ARG;
   if (s->batch == 0) return FFD_OK;
+  // one block of the merge a row
+  if (static_cast<int64_t>(s->batch) * num_nodes * s->num_q_heads >= (int64_t{1} << 31)) return FFD_ERR_UNSUPPORTED;
   const int group = s->num_q_heads / s->num_kv_heads;
   const TreeLayout L = tree_layout(s->batch, s->num_kv_heads, group, num_nodes, s->capacity);
   if (workspace == nullptr || workspace_bytes < L.total) return FFD_ERR_WORKSPACE;

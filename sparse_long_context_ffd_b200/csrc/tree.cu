@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
           }
         }
       }
-      if (*dead)  // what is in flight lands before the CTA ends
+      // what is in flight lands before the CTA ends, whoever gave up
         for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
           mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
     }
@@ -243,10 +243,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       }
       n += g.tiles;
     }
-    if (*dead) {  // what was issued is done before tensor memory is given back
-      if (elect_one()) mma_commit(bar_end);
-      mbar_wait(bar_end, 0, kWaitLimitNs);
-    }
+    // what was issued is done before tensor memory is given back, whoever gave up
+    if (elect_one()) mma_commit(bar_end);
+    __syncwarp();
+    mbar_wait(bar_end, 0, kWaitLimitNs);
     }
   } else {
     // ------------------------------------------------------------- softmax --
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             tmem_st<kPart / 2>(tm_s + (part * kCols + c0) / 2, w);
           }
         };
-        if (kByte || masked) {
+        if (kByte || masked || __any_sync(0xFFFFFFFFu, m == -INFINITY)) {
           weigh(0, x, true);
           if constexpr (kCols > kPart) {
             load(kPart, x);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       }
     }
     __syncwarp();
-    if (*dead)  // what is in flight lands before the CTA ends
+    // what is in flight lands before the CTA ends, whoever gave up
       for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
         mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
   } else if (warp == kMatrixWarp) {
@@ -238,10 +238,10 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       }
       n += g.tiles;
     }
-    if (*dead) {  // what was issued is done before tensor memory is given back
-      if (elect_one()) mma_commit(bar_end);
-      mbar_wait(bar_end, 0, kWaitLimitNs);
-    }
+    // what was issued is done before tensor memory is given back, whoever gave up
+    if (elect_one()) mma_commit(bar_end);
+    __syncwarp();
+    mbar_wait(bar_end, 0, kWaitLimitNs);
   } else if (warp < kMatrixWarp) {
     // ------------------------------------------------------------- softmax --
     const int s = warp >> 2, w = warp & 3;       // group; which 32 lanes of an accumulator

@@ -146,6 +146,7 @@ def test_tree_refusals():
                 *({"c": c} for c in BAD_CACHES)):
         assert call(**bad) == INVALID, bad
     assert call(ws=None) == WORKSPACE and call(wb=need - 1) == WORKSPACE
+    assert call(s=ffd.make_shape(65535, 4096, 512, 64, 64, 16), n=64, wb=1 << 60) == UNSUPPORTED
     assert call(s=ffd.make_shape(0, 16, 4, 4096, 64, 16), c=None) == ffd.FFD_OK
     assert lib.ffd_decode_tree_workspace_bytes(ctypes.byref(SHAPE), 0) == 0
     assert lib.ffd_decode_tree_workspace_bytes(ctypes.byref(SHAPE), 65) == 0
