@@ -1,9 +1,11 @@
 // rows.cu -- rotary positions, the cache write of several tokens a sequence,
 // and the 8-bit cache read back.
 //
-// All three pass once over rows of 128 channels and are bound by HBM (at large
-// token counts) or by launch latency (at small ones); the arithmetic only has
-// to stay out of the way.
+// All three pass once over rows of 128 channels.  At small counts they are the
+// launch and the host's call (16 tokens: 7.6 us a call back to back).  At large
+// ones rotation and read-back are near HBM's rate (8191 tokens x 40 heads: 33 us,
+// 5.1 TB/s; read-back 5.4 to 5.8), and the 8-bit write is bound by instruction
+// issue (32K tokens: 174 us, 4.2 TB/s, 65% of issue slots taken).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

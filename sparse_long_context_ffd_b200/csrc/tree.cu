@@ -8,14 +8,27 @@
 //
 // The work of a call is one list of 128-token tiles, (sequence, kv-head, rows)
 // after another, cut into equal parts, one for each CTA: long sequences are
-// split, short ones share a CTA, whatever the lengths are.  Parts of a unit
-// are joined by merge_kernel, in the order of the CTAs.
+// split, short ones share a CTA, whatever the lengths are (or, see find_part,
+// each unit into its own).  Parts of a unit are joined by merge_tree_kernel, in
+// the order of the CTAs.
 //
 // A CTA: two groups of 128 softmax threads, one thread that issues the copies
 // and one that issues the matrix instructions.  Up to 128 rows, the groups
 // take alternate tiles with an accumulator each; more, they take 128 rows each
 // of the same tiles.  Either way the tensor cores work for one group while the
 // other does its exponentials.
+//
+// What bounds it: a group's chain of a tile.  With 2 x 128 rows (64 nodes, 3
+// sequences of up to 16K tokens, 60 us) it is 1600 clocks of exponentials, two
+// products of 512 each that wait 300 to 700 for the other group's, and 300 until
+// the answer is seen: 4300 for a pair of tiles, of which the tensor cores work
+// 2048.  With 64 rows over bf16 (16 nodes, 128K tokens, 105 us, 5.1 TB/s) the
+// tiles come at 85% of the copy's rate in between, and the start, the last parts
+// and the merge take 15 us.  Over e4m3 (13 nodes, 5 sequences of up to 64K, 146 us)
+// the two parts of queries and weights make two products of each, at half the
+// bytes: the chain, 3000 clocks a tile, sets the pace.  One matrix warp for each
+// group, as they please or under a lock, was slower (both groups fall into step:
+// 74 and 69 us where one warp took 67), and so were two threads a row (95 us).
 //
 // bf16 cache: P has bf16's 8 significant bits.  8-bit cache: codes enter the
 // matrix instructions as they are.  The query row, scaled by a power of two
