@@ -103,18 +103,13 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// N (4, 8, 16 or 32) consecutive columns of the thread's lane; complete after tmem_wait_ld.
+// N (4, 16 or 32) consecutive columns of the thread's lane; complete after tmem_wait_ld.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float *v) {
-  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+  static_assert(N == 4 || N == 16 || N == 32, "columns");
   if constexpr (N == 4)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                 : "r"(addr)
-                 : "memory");
-  else if constexpr (N == 8)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(addr)
                  : "memory");
   else if constexpr (N == 16)
@@ -144,15 +139,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float *v) {
 // the same wait) of nothing: no use of them can be moved ahead of it.
 template <int N, bool kWait = true>
 __device__ __forceinline__ void tmem_wait_ld(float *v) {
-  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+  static_assert(N == 4 || N == 16 || N == 32, "columns");
   if constexpr (N == 4 && kWait)
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3])::"memory");
   else if constexpr (N == 4 && !kWait)
     asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3])::"memory");
-  else if constexpr (N == 8 && kWait)
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
-  else if constexpr (N == 8 && !kWait)
-    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
   else if constexpr (N == 16 && kWait)
     asm volatile(
         "tcgen05.wait::ld.sync.aligned;"
@@ -181,16 +172,11 @@ __device__ __forceinline__ void tmem_wait_ld(float *v) {
       "+f"(v[31])::"memory");
 }
 
-// N (4, 8, 16 or 32) consecutive columns; complete after tmem_wait_st.
+// N (8, 16 or 32) consecutive columns; complete after tmem_wait_st.
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t *v) {
-  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
-  if constexpr (N == 4)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
-        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
-  else if constexpr (N == 8)
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 8)
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
         ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
   volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
   int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
 
-  asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
   if (tid == 8 * 32) {  // (warp 0 divides the work meanwhile)
     for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
@@ -111,6 +110,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     prefetch_tmap(&tmap_v);
     if (!kByte) prefetch_tmap(&tmap_q);
   }
+  // (nothing of the stream's earlier work is read or written before this; the
+  // merge may start then, and reads lengths and sizes at once)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   find_part<kCtaThreads>(p, reinterpret_cast<int *>(row_s), start_s);
   tc_fence_before();
   __syncthreads();
@@ -680,6 +683,7 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   const int b = bi / p.nodes, i = bi - b * p.nodes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t *out = p.out + static_cast<size_t>(blockIdx.x) * kHeadDim;
+  asm volatile("griddepcontrol.launch_dependents;");
   const Sequence q(p, b);  // (an input, not something the kernel before leaves)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!q.good) {
@@ -800,8 +804,7 @@ cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUten
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_kernel<kByte, kCols, kPair><<<p.ctas, kCtaThreads, L::kTotal, stream>>>(map_k, map_v, map_q, p);
-  return cudaGetLastError();
+  return launch_early(tree_kernel<kByte, kCols, kPair>, p.ctas, kCtaThreads, L::kTotal, stream, map_k, map_v, map_q, p);
 }
 
 cudaError_t launch_rows_of(const TreeParams &p, cudaStream_t stream) {
@@ -842,18 +845,9 @@ cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream) {
     const cudaError_t e = launch_rows_of(p, stream);
     if (e != cudaSuccess) return e;
   }
-  // (starts while the kernel before it ends, and waits for it on the GPU)
-  cudaLaunchAttribute attribute{};
-  attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attribute.val.programmaticStreamSerializationAllowed = p.ctas > 0 ? 1 : 0;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(static_cast<unsigned>(p.batch) * static_cast<unsigned>(p.nodes) *
-                        static_cast<unsigned>(p.kv_heads << p.group_log2));
-  config.blockDim = dim3(128);
-  config.stream = stream;
-  config.attrs = &attribute;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, merge_tree_kernel, p);
+  const dim3 rows(static_cast<unsigned>(p.batch) * static_cast<unsigned>(p.nodes) *
+                  static_cast<unsigned>(p.kv_heads << p.group_log2));
+  return launch_early(merge_tree_kernel, rows, 128, 0, stream, p);
 }
 
 }  // namespace ffd

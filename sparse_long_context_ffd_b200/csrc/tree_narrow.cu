@@ -107,7 +107,6 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
   int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
   constexpr int kMatrixWarp = kGroups * kGroup / 32, kCopyWarp = kMatrixWarp + 1;
 
-  asm volatile("griddepcontrol.launch_dependents;");
   if (warp == kMatrixWarp) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), L::kTmem);
   if (tid == kCopyWarp * 32) {  // (warp 0 divides the work meanwhile)
     for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bars + i, 1);
@@ -124,6 +123,10 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
+  // (nothing of the stream's earlier work is read or written before this; the
+  // merge may start then, and reads lengths and sizes at once)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   find_part<L::kThreads>(p, reinterpret_cast<int *>(warp_row_s), start_s);
   tc_fence_before();
   __syncthreads();
@@ -555,8 +558,7 @@ cudaError_t launch_as(const TreeParams &p, const CUtensorMap &map_k, const CUten
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  tree_narrow_kernel<kByte><<<p.ctas, L::kThreads, L::kTotal, stream>>>(map_k, map_v, p);
-  return cudaGetLastError();
+  return launch_early(tree_narrow_kernel<kByte>, p.ctas, L::kThreads, L::kTotal, stream, map_k, map_v, p);
 }
 
 }  // namespace

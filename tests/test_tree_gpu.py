@@ -333,3 +333,29 @@ def test_long_cache_row_tiles(fmt, n, G):
             want, mag = p @ vv, p @ vv.abs()
             tol = want.abs() * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -10)
             assert ((out[b, :, h].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt,n", [(f, n) for f in FORMATS for n in (2, 20)])
+def test_behind_and_before_other_work_in_a_graph(fmt, n):
+    """Inputs that a copy, a fill and a kernel of the same graph leave just
+    before the call, results that one takes just after it; twice in a row."""
+    c = Case(fmt, 2, n, 4, 2, 1024, [900, 333], seed=30).device()
+    want = c.run()
+    q, lengths = c.q.cuda(), c.d_lengths.clone()
+    late_q, late_lengths, after = torch.zeros_like(q), torch.zeros_like(lengths), [torch.zeros_like(c.out) for _ in range(2)]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for i in range(2):
+            late_lengths.zero_()
+            late_q.copy_(q)
+            torch.add(late_lengths, lengths, out=late_lengths)
+            ffd.decode_tree(c.shape, c.cache, late_q, late_lengths, c.out, c.ws, tree_mask=c.mask)
+            after[i].copy_(c.out)
+            late_q.zero_()
+    for _ in range(3):
+        for t in (c.out, *after):
+            t.zero_()
+        graph.replay()
+        for t in after:
+            assert torch.equal(t.cpu().view(torch.int16), want.view(torch.int16))
