@@ -2,10 +2,11 @@
 // and the 8-bit cache read back.
 //
 // All three pass once over rows of 128 channels.  At small counts they are the
-// launch and the host's call (16 tokens: 7.6 us a call back to back).  At large
-// ones rotation and read-back are near HBM's rate (8191 tokens x 40 heads: 33 us,
-// 5.1 TB/s; read-back 5.4 to 5.8), and the 8-bit write is bound by instruction
-// issue (32K tokens: 174 us, 4.2 TB/s, 65% of issue slots taken).
+// launch and the host's call (16 tokens: 6.8 us a call back to back; a kernel may
+// start while the one before it ends, 7.6 without).  At large ones rotation and
+// read-back are near HBM's rate (8191 tokens x 40 heads: 32 us, 5.3 TB/s; read-back
+// 5.5 to 5.8), and the 8-bit write is bound by instruction issue (32K tokens: 173
+// us, 4.3 TB/s, 65% of issue slots taken).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -79,6 +80,8 @@ __global__ void __launch_bounds__(kThreads, kByte ? 4 : 5) rows_kernel(const __g
   __shared__ RowPlace place_s[kTableRows];
   __shared__ uint16_t *scale_s[kByte ? kTableRows : 1];
   __shared__ uint8_t kind_s[kTableRows];  // 0 query, 1 key, 2 value
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int half = p.rotary_dim >> 1;
   const int token0 = blockIdx.x * tokens_a_block;
   const int tokens_here = min(tokens_a_block, p.tokens - token0);
@@ -260,13 +263,15 @@ __global__ void __launch_bounds__(kThreads, kByte ? 4 : 5) rows_kernel(const __g
 
 // Sixteen codes (16 bytes in, 32 out) a thread; code * scale is exact in fp32 (4
 // and 8 significant bits), so the only rounding is the one to bf16.  Bound by HBM
-// (4 x 8 x 32768 tokens: 140 us, 5.8 TB/s; 18 MB: 7.2 us).  One row a thread and
+// (4 x 8 x 32768 tokens: 140 to 146 us, 5.5 to 5.8 TB/s; 18 MB: 5.8 us).  One row a thread and
 // more blocks beat several rows in flight a thread: 2, 4 and 8 of them took 141,
-// 144 and 154 us, and 8.1, 8.2 and 9.0 us of the 18 MB.
+// 144 and 154 us, and of the 18 MB 8.1, 8.2 and 9.0 us where one took 7.2.
 constexpr int kReadLanes = 8;  // threads of a row
 constexpr int kReadAtOnce = kThreads / kReadLanes;
 
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const bool values = blockIdx.y != 0;
   uint16_t *out = values ? p.out[1] : p.out[0];
   const uint8_t *codes = values ? p.codes[1] : p.codes[0];
@@ -311,8 +316,7 @@ cudaError_t launch_rows_as(const RowsParams &p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.tokens + tokens_a_block - 1) / tokens_a_block),
                   static_cast<unsigned>((rows + rows_a_block - 1) / rows_a_block));
   const size_t smem = static_cast<size_t>(tokens_a_block) * (p.rotary_dim / 2) * sizeof(float2);
-  rows_kernel<kAppend, kByte><<<grid, kThreads, smem, stream>>>(p, tokens_a_block, rows_a_block);
-  return cudaGetLastError();
+  return launch_early(rows_kernel<kAppend, kByte>, grid, kThreads, smem, stream, p, tokens_a_block, rows_a_block);
 }
 
 }  // namespace
@@ -324,8 +328,7 @@ cudaError_t launch_rows(const RowsParams &p, bool append, int format, cudaStream
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.count + kReadAtOnce - 1) / kReadAtOnce) * static_cast<unsigned>(p.batch * p.kv_heads), 2);
-  read_kernel<<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(read_kernel, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace ffd

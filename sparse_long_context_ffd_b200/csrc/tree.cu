@@ -19,12 +19,12 @@
 // other does its exponentials.
 //
 // What bounds it: a group's chain of a tile.  With 2 x 128 rows (64 nodes, 3
-// sequences of up to 16K tokens, 60 us) it is 1600 clocks of exponentials, two
+// sequences of up to 16K tokens, 58 us) it is 1600 clocks of exponentials, two
 // products of 512 each that wait 300 to 700 for the other group's, and 300 until
 // the answer is seen: 4300 for a pair of tiles, of which the tensor cores work
-// 2048.  With 64 rows over bf16 (16 nodes, 128K tokens, 105 us, 5.1 TB/s) the
+// 2048.  With 64 rows over bf16 (16 nodes, 128K tokens, 103 us, 5.2 TB/s) the
 // tiles come at 85% of the copy's rate in between, and the start, the last parts
-// and the merge take 15 us.  Over e4m3 (13 nodes, 5 sequences of up to 64K, 146 us)
+// and the merge take 13 us.  Over e4m3 (13 nodes, 5 sequences of up to 64K, 143 us)
 // the two parts of queries and weights make two products of each, at half the
 // bytes: the chain, 3000 clocks a tile, sets the pace.  One matrix warp for each
 // group, as they please or under a lock, was slower (both groups fall into step:

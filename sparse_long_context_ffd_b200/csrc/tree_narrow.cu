@@ -13,10 +13,10 @@
 //
 // Groups of 128 threads take the tiles in turn, with an S and an O each.
 //
-// One token of 4 sequences x 32K over e4m3 (4 rows): 63 us, 4.3 TB/s, where the
+// One token of 4 sequences x 32K over e4m3 (4 rows): 60 us, 4.5 TB/s, where the
 // kernel with rows as lanes took 80; the issue of the products (about 900 clocks a
 // tile, of which they run 320) sets the pace against 1290 that the bytes take at
-// the copy's rate, and the start and the merge add 12 us.  With 32 and 64 rows
+// the copy's rate, and the start and the merge add 10 us.  With 32 and 64 rows
 // this form was slower than the other (190 us where it took 146: every weight of
 // every column passes one thread's arithmetic).
 #include <atomic>
