@@ -16,6 +16,17 @@ constexpr float kScoreScale = 0.08838834764831845f * 1.4426950408889634f;  // lo
 
 __device__ __forceinline__ float bf16_f(uint32_t b) { return __uint_as_float(b << 16); }
 
+// A running reference in units of log 2.  Weights are 2^(s - m), s exact and m a
+// score rounded to fp32: all of a row's are off by the factor that m is, which its
+// sum shares.  In bf16 that may be 2^64, at 2^30.  In e4m3 it must stay within the
+// 7% between 448, where m moves, and 480, which is NaN's code; at 2^19 the score's
+// and the border's roundings make 2% of it.  A row beyond that is NaN, not a
+// number that is wrong.
+template <bool kByte>
+__device__ __forceinline__ float in_range(float m) {
+  return fabsf(m) > (kByte ? 0x1p19f : 0x1p30f) && m != -INFINITY ? __uint_as_float(0x7FFFFFFFu) : m;
+}
+
 __device__ __forceinline__ float exp2_f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         constexpr float kRoom = kByte ? 8.8f - 7.0f : 8.0f;
         if constexpr (kByte) high -= 7.0f; else high *= kScoreScale;
         if (j < 2 && (kPair ? j == 0 : true)) {
-          m = high;
+          m = in_range<kByte>(high);
         } else if (__any_sync(0xFFFFFFFFu, high > m + kRoom)) {
-          const float next = fmaxf(m, high);
+          const float next = in_range<kByte>(fmaxf(m, high));
           const float f = next == m ? 1.0f : exp2_f(m - next);
           m = next;
           l *= f;

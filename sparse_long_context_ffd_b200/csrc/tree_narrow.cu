@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
           if (r < kRows) {
             const float *of = warp_row_s + 4 * s * kRows + r;
             const float high = fmaxf(fmaxf(of[0], of[kRows]), fmaxf(of[2 * kRows], of[3 * kRows]));
-            const float m = ref[r], next = high > m + kRoom ? high - kAbove : m;
+            const float m = ref[r], next = high > m + kRoom ? in_range<kByte>(high - kAbove) : m;
             ref[r] = next;
             fade[r] = next == m ? 1.0f : exp2_f(m - next);
           }
