@@ -555,8 +555,7 @@ ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const 
  * the softmax weights enter the product with V with 8 significant bits.  Over an
  * FFD_CACHE_BYTE cache so do the weights times V's scales, in units no coarser
  * than 2^-16 of the largest one met so far, and the queries, in units no coarser
- * than 2^-16 of the largest magnitude in the row (with at most 16 query rows a
- * kv-head, num_nodes * Hq / Hkv: 2^-20 of the largest in any of them).
+ * than 2^-16 of the largest magnitude in the row.
  * A row whose scores pass 2^29 in magnitude (over an FFD_CACHE_BYTE cache 2^18),
  * more than fp32 tells apart well enough, may be NaN.
  * A sequence whose length is outside [0, cap], or whose size is outside [0,

@@ -54,7 +54,7 @@ struct Narrow {
   static constexpr int kFade = kRef + kGroups * kRows * 4;  // [group][kRows]
   static constexpr int kWarpRow = kFade + kGroups * kRows * 4;  // [group][4 warps][kRows]
   static constexpr int kSeen = kWarpRow + kGroups * 4 * kRows * 4;  // [kRows]
-  static constexpr int kTot = kSeen + kRows * 8;            // [kRows] (m, sum); largest query magnitudes
+  static constexpr int kTot = kSeen + kRows * 8;            // [kRows] (m, sum); before, scales of the query rows
   static constexpr int kBars = kTot + kRows * 8;
   static constexpr int kNumBars = 2 * kSlots + 3 * kGroups + 2;
   static constexpr int kWords = kBars + kNumBars * 8;
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
   float *fade_s = reinterpret_cast<float *>(smem + L::kFade);
   float *warp_row_s = reinterpret_cast<float *>(smem + L::kWarpRow);
   float2 *tot_s = reinterpret_cast<float2 *>(smem + L::kTot);
+  float *row_scale_s = reinterpret_cast<float *>(tot_s);  // of the query rows, until a segment's end (e4m3)
   uint64_t *seen_s = reinterpret_cast<uint64_t *>(smem + L::kSeen);
   volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
   volatile int *dead = words + 1;      // a wait ran out
@@ -273,10 +274,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       const int first = g.len - g.size;
       const int bh = g.b * p.kv_heads + head;
       // ---- the query rows: 16 threads a row, all loads before the first use ----
-      // e4m3: all rows are scaled by one power of two, the largest magnitude into
-      // [128, 256).  (What a small row loses is below what a large one's scores
-      // are off by; a softmax goes by differences.)
-      float score_scale = kScoreScale;
+      // e4m3: each row is scaled by a power of two, its largest magnitude into [128, 256).
       {
         const int c = tid & 15, r = tid >> 4, i = r >> p.group_log2;
         uint4 x = make_uint4(0, 0, 0, 0);
@@ -293,17 +291,9 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
           for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
 #pragma unroll
           for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-          uint32_t most = top < 0x7F80u ? top : 0;
-          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
-          uint32_t *most_s = reinterpret_cast<uint32_t *>(tot_s);
-          if (lane == 0) most_s[warp] = most;
-          named_barrier(bar_all, kGroups * kGroup);
-          most = 0;
-#pragma unroll
-          for (int e = 0; e < kRows / 2; ++e) most = max(most, most_s[e]);
-          const int exponent = most == 0 ? 0 : min(100, 134 - static_cast<int>(most >> 7));
-          score_scale *= __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-          const float by = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 + exponent) << 23 : 0x7FFFFFFFu);  // (an infinity spoils its row)
+          const int exponent = top == 0 ? 0 : min(100, 134 - static_cast<int>(top >> 7));
+          const float by = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -313,6 +303,8 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
             uint8_t *dst = smem + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
             *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2 *>(dst + kRows * 128) = make_uint2(lo[0], lo[1]);
+            // (an infinity spoils its row)
+            if (c == 0) row_scale_s[r] = top < 0x7F80u ? kScoreScale * down : __uint_as_float(0x7FFFFFFFu);
           }
         } else {
           *reinterpret_cast<uint4 *>(smem + r * 128 + (c >> 3) * kRows * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
@@ -334,9 +326,9 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
         const uint32_t vi = 2 * (n + j) + 1, v_slot = vi % kSlots, k_slot = (vi - 1) % kSlots;
         wait(bar_s + s, count & 1);
         tc_fence_after();
-        float ks = score_scale, vs = 1.0f, lv = 0.0f;
+        float ks = kScoreScale, vs = 1.0f, lv = 0.0f;
         if constexpr (kByte) {
-          ks *= bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + k_slot * 256)[t]);
+          ks = bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + k_slot * 256)[t]);
           wait(full + v_slot, (vi / kSlots) & 1);
           vs = bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + v_slot * 256)[t]);
           if (masked && token >= first) {
@@ -367,10 +359,18 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 m = below(e);
-            x[e] = fmaf(x[e], ks, -m.x);
-            x[e + 1] = fmaf(x[e + 1], ks, -m.y);
-            x[e + 2] = fmaf(x[e + 2], ks, -m.z);
-            x[e + 3] = fmaf(x[e + 3], ks, -m.w);
+            if constexpr (kByte) {
+              const float4 rs = *reinterpret_cast<const float4 *>(row_scale_s + e);
+              x[e] = fmaf(x[e] * ks, rs.x, -m.x);
+              x[e + 1] = fmaf(x[e + 1] * ks, rs.y, -m.y);
+              x[e + 2] = fmaf(x[e + 2] * ks, rs.z, -m.z);
+              x[e + 3] = fmaf(x[e + 3] * ks, rs.w, -m.w);
+            } else {
+              x[e] = fmaf(x[e], ks, -m.x);
+              x[e + 1] = fmaf(x[e + 1], ks, -m.y);
+              x[e + 2] = fmaf(x[e + 2], ks, -m.z);
+              x[e + 3] = fmaf(x[e + 3], ks, -m.w);
+            }
           }
           if (masked && token >= first) {
             const int at = token - first;
