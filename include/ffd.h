@@ -560,7 +560,9 @@ ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const 
  * more than fp32 tells apart well enough, may be NaN.
  * A sequence whose length is outside [0, cap], or whose size is outside [0,
  * min(num_nodes, length)], yields zero rows (all num_nodes) and sets
- * FFD_DEVICE_FLAG_BAD_LENGTH in the workspace (ffd_check_device_status).
+ * FFD_DEVICE_FLAG_BAD_LENGTH in the workspace (ffd_check_device_status); a wait
+ * inside the kernel that runs out (after 2 s) sets FFD_DEVICE_FLAG_TIMEOUT, and the
+ * call's results are void.
  * 1 <= num_nodes <= FFD_MAX_TREE_NODES, B * num_nodes * Hq < 2^31.  The result
  * does not depend on what the workspace held.  Calls that share a workspace
  * must not overlap on the GPU. */

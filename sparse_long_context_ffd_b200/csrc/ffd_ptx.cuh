@@ -108,15 +108,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 // The same in five instructions, bounded by a count of attempts (each may rest
 // up to a microsecond): for warps that share an instruction cache with long
 // unrolled code and wait often.
+template <uint32_t kAttempts>
 __device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 4194304;\n"
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
       "again:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t@p bra over;\n\t"
       "sub.u32 n, n, 1;\n\tsetp.ne.u32 p, n, 0;\n\t@p bra again;\n"
       "over:\n\tmov.u32 %0, n;\n\t}"
       : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "r"(smem_addr(bar)), "r"(parity), "n"(kAttempts)
       : "memory");
   return done != 0;
 }

@@ -75,6 +75,7 @@ struct TreeParams {
   float *partials;              // [ctas][2][part_floats(rows)]
   int32_t batch, kv_heads, group_log2, nodes, capacity, format;
   int32_t units_a_head, rows, ctas;
+  uint64_t wait_limit_ns;
 };
 
 struct TreeLayout {

@@ -127,6 +127,41 @@ __device__ __forceinline__ void split4_signed(float w0, float w1, float w2, floa
   lo |= signs;
 }
 
+// ------------------------------------------------------------------ waits --
+
+// A CTA's waits, in shared memory.  After one of them ran out nobody waits any more:
+// copies and matrix instructions stop, and the softmax threads, whose barriers count
+// on one another, go through the rest of their work on whatever is there.
+struct Waits {
+  volatile int dead;  // a wait was given up
+  uint32_t *err;
+  uint64_t limit_ns;
+};
+
+#ifdef FFD_DEBUG
+constexpr uint32_t kAttempts = 1;
+#else
+constexpr uint32_t kAttempts = 4096;  // a few milliseconds at most
+#endif
+
+// Whether to go on; else the CTA's waits are over.
+__device__ __forceinline__ bool keep_waiting(Waits *w, uint64_t start) {
+  if (w->dead == 0 && global_timer_ns() - start > w->limit_ns) {
+    w->dead = 1;
+    atomicOr(w->err, kFlagTimeout);
+  }
+  return w->dead == 0;
+}
+
+// A wait whose first attempts were in vain.  (Apart: inlined at every wait, one token
+// over 4 x 32768 in 8 bits took 63 us instead of 62.)
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, Waits *w) {
+  const uint64_t start = global_timer_ns();
+  while (keep_waiting(w, start))
+    if (mbar_wait_short<kAttempts>(bar, parity)) return true;
+  return false;
+}
+
 // ------------------------------------------------------------------- work --
 
 struct Sequence {

@@ -13,6 +13,13 @@ namespace {
 
 constexpr size_t kErrBytes = 256;  // the error word at the head of a workspace
 
+// The limit of ffd_decode_tree's waits on the device; the debug library can shorten it.
+#ifdef FFD_DEBUG
+uint64_t g_wait_limit_ns = kWaitLimitNs;
+#else
+constexpr uint64_t g_wait_limit_ns = kWaitLimitNs;
+#endif
+
 struct Range {
   const void *p;
   size_t bytes;
@@ -234,6 +241,12 @@ ffd_status ffd_read_cache(const ffd_shape *s, const ffd_cache *c, const int32_t 
   return launch_read(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? FFD_OK : FFD_ERR_CUDA;
 }
 
+#ifdef FFD_DEBUG
+// Debug library only (not in the public header): the limit of the following calls'
+// waits.
+void ffd_debug_tree_wait_limit(uint64_t ns) { g_wait_limit_ns = ns; }
+#endif
+
 size_t ffd_decode_tree_workspace_bytes(const ffd_shape *s, int32_t num_nodes) {
   if (check_shape(s) != FFD_OK || num_nodes < 1 || num_nodes > FFD_MAX_TREE_NODES) return 0;
   return tree_layout(s->batch, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, num_nodes, s->capacity).total;
@@ -309,6 +322,7 @@ ffd_status ffd_decode_tree(const ffd_shape *s, const ffd_cache *c, int32_t num_n
   p.nodes = num_nodes;
   p.capacity = s->capacity;
   p.format = c->format;
+  p.wait_limit_ns = g_wait_limit_ns;
   return launch_tree(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? FFD_OK : FFD_ERR_CUDA;
 }
 

@@ -64,7 +64,7 @@ struct Layout {
   static constexpr int kBars = kScale + (kByte ? 2 * kGroup * 4 : 0);
   static constexpr int kNumBars = 2 * kSlots + 8;
   static constexpr int kWords = kBars + kNumBars * 8;
-  static constexpr int kTotal = kWords + 32;
+  static constexpr int kTotal = kWords + 32 + sizeof(Waits);
   static_assert(kTotal <= kSmemMax, "shared memory");
 };
 
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
   uint64_t *full = bars, *empty = bars + kSlots;
   uint64_t *bar_s = empty + kSlots, *bar_p = bar_s + 2, *bar_o = bar_s + 4, *bar_q = bar_s + 6;
   uint64_t *bar_end = bar_s + 7;
+  Waits *waits = reinterpret_cast<Waits *>(smem + L::kWords + 32);
   volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
-  volatile int *dead = words + 1;      // a wait ran out
-  volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
-  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
+  volatile int *odd = words + 1;       // a value in a drafted token's row is not finite
+  int *start_s = const_cast<int *>(words) + 2;  // b, offset, tiles, all tiles
 
   if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
   if (tid == 8 * 32) {  // (warp 0 divides the work meanwhile)
@@ -104,7 +104,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     mbar_init(bar_q, kByte ? 2 * kGroup : 1);
     mbar_init(bar_end, 1);
     fence_mbar_init();
-    *dead = 0;
+    waits->dead = 0;
+    waits->err = p.err;
+    waits->limit_ns = p.wait_limit_ns;
     *odd = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
@@ -126,14 +128,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
   // together again (they leave a wait one by one, and elect_one and the
   // instructions under it are for a converged warp).
   auto all = [](bool b) { return __all_sync(0xFFFFFFFFu, b) != 0; };
-  // After one wait ran out nobody waits, loads or multiplies any more.
-  bool alive = true;
+  bool alive = true;  // no wait of this thread was given up
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (alive && !mbar_wait_short(bar, parity)) {
-      alive = false;
-      *dead = 1;
-      atomicOr(p.err, kFlagTimeout);
-    }
+    if (alive && !mbar_wait_short<kAttempts>(bar, parity)) alive = wait_on(bar, parity, waits);
     return alive;
   };
 
@@ -163,7 +160,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
         for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
           const uint32_t slot = i % kSlots, round = i / kSlots;
-          if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1));
+          // (a slot given back by a thread that waits no more may still be filling)
+          if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1) && waits->dead == 0);
           if (!alive) break;
           const int t0 = (g.tile0 + (j >> 1)) * kTile;
           const int row = bh * p.capacity + t0;
@@ -210,6 +208,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       ++segments;
       int si = 0, oi = 0;  // items whose S, whose O have gone out
       uint32_t spin = 0;
+      uint64_t since = 0;
 #pragma unroll 1
       while (alive && oi < items) {
         const uint32_t sg = uniform(si & 1), og = uniform(oi & 1);
@@ -221,11 +220,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         const bool do_o = (yes & 6u) == 6u && oi < si;
         const bool do_s = (yes & 1u) != 0 && si < items && si < oi + (do_o ? 3 : 2);
         if (!do_s && !do_o) {
-          if (++spin < (1u << 23)) continue;
-          alive = false;
-          *dead = 1;
-          if (lane == 0) atomicOr(p.err, kFlagTimeout);
-          break;
+          if ((++spin & (kAttempts - 1)) != 0) continue;
+          if (spin == kAttempts) since = global_timer_ns();
+          alive = all(keep_waiting(waits, since));
+          continue;
         }
         spin = 0;
         tc_fence_after();
@@ -274,6 +272,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t tm_s = tmem + lanes + 128 * s, tm_o = tmem + lanes + 256 + 128 * s;
     uint32_t s_count = 0, o_count = 0, n = 0;
+    uint32_t queries = 0;                        // tiles of query rows asked for (bf16; thread 0)
     bool starts = true;                          // the CTA's first segment
     while (walk.next(p, g)) {
       const int head = g.unit / p.units_a_head;
@@ -333,8 +332,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar_q);
-      } else if (tid == 0 && !starts) {  // (the first segment's: the copy warp, before K and V)
-        load_query(g);
+      } else if (tid == 0) {  // (the first segment's: the copy warp, before K and V)
+        if (!starts && alive) load_query(g);
+        if (alive) ++queries;
       }
 
       // ---- the tiles ----
@@ -660,6 +660,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       if (tid == 0) *odd = 0;
     }
     if (t == 0) bulk_wait<0>();
+    // (the products waited for them, but may have been given up)
+    if (queries > 0) mbar_wait(bar_q, (queries - 1) & 1, kWaitLimitNs);
   }
   __syncwarp();
   tc_fence_before();
@@ -695,8 +697,8 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   const int row = (i << p.group_log2) + (head & ((1 << p.group_log2) - 1));
   const int kv = head >> p.group_log2, block = row / kTreeRows;
   const int2 at = p.table[(static_cast<size_t>(b) * p.kv_heads + kv) * p.units_a_head + block];
-  // (a part count beyond the grid can only be left over from a call that gave up)
-  if (at.y <= 1 || at.x < 0 || (at.x >> 1) + at.y > p.ctas) return;
+  // (every call writes its entries, one that gave up too; no other is followed)
+  if (at.y <= 1 || at.y > p.ctas || at.x < 0 || (at.x >> 1) > p.ctas - at.y) return;
   const size_t slot = part_floats(p.rows);
   // part 0 is in the slot that the table names, the others begin their CTAs: slot 0
   const int r0 = row - block * kTreeRows;

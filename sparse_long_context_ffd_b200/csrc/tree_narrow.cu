@@ -58,7 +58,7 @@ struct Narrow {
   static constexpr int kBars = kTot + kRows * 8;
   static constexpr int kNumBars = 2 * kSlots + 3 * kGroups + 2;
   static constexpr int kWords = kBars + kNumBars * 8;
-  static constexpr int kTotal = kWords + 32;
+  static constexpr int kTotal = kWords + 32 + sizeof(Waits);
   static_assert(kTotal <= kSmemMax, "shared memory");
   // (even: a slot then holds K's only or V's only, as `idle` below needs)
   static_assert(kSlots >= 2 * kGroups && kSlots % 2 == 0, "the ring would stop");
@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
   float2 *tot_s = reinterpret_cast<float2 *>(smem + L::kTot);
   float *row_scale_s = reinterpret_cast<float *>(tot_s);  // of the query rows, until a segment's end (e4m3)
   uint64_t *seen_s = reinterpret_cast<uint64_t *>(smem + L::kSeen);
+  Waits *waits = reinterpret_cast<Waits *>(smem + L::kWords + 32);
   volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
-  volatile int *dead = words + 1;      // a wait ran out
-  volatile int *odd = words + 2;       // a value in a drafted token's row is not finite
-  int *start_s = const_cast<int *>(words) + 3;  // b, offset, tiles, all tiles
+  volatile int *odd = words + 1;       // a value in a drafted token's row is not finite
+  int *start_s = const_cast<int *>(words) + 2;  // b, offset, tiles, all tiles
   constexpr int kMatrixWarp = kGroups * kGroup / 32, kCopyWarp = kMatrixWarp + 1;
 
   if (warp == kMatrixWarp) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), L::kTmem);
@@ -119,7 +119,9 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     mbar_init(bar_q, kGroups * kGroup);
     mbar_init(bar_end, 1);
     fence_mbar_init();
-    *dead = 0;
+    waits->dead = 0;
+    waits->err = p.err;
+    waits->limit_ns = p.wait_limit_ns;
     *odd = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
@@ -140,14 +142,9 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
   // together again (they leave a wait one by one, and elect_one and the
   // instructions under it are for a converged warp).
   auto all = [](bool b) { return __all_sync(0xFFFFFFFFu, b) != 0; };
-  // After one wait ran out nobody waits, loads or multiplies any more.
-  bool alive = true;
+  bool alive = true;  // no wait of this thread was given up
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (alive && !mbar_wait_short(bar, parity)) {
-      alive = false;
-      *dead = 1;
-      atomicOr(p.err, kFlagTimeout);
-    }
+    if (alive && !mbar_wait_short<kAttempts>(bar, parity)) alive = wait_on(bar, parity, waits);
     return alive;
   };
 
@@ -159,7 +156,8 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       const int bh = g.b * p.kv_heads + g.unit;
       for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
         const uint32_t slot = i % kSlots, round = i / kSlots;
-        if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1));
+        // (a slot given back by a thread that waits no more may still be filling)
+        if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1) && waits->dead == 0);
         if (!alive) break;
         const int t0 = (g.tile0 + (j >> 1)) * kTile;
         const int row = bh * p.capacity + t0;
@@ -201,6 +199,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
       ++segments;
       int si = 0, oi = 0;  // tiles whose S, whose O have gone out
       uint32_t spin = 0;
+      uint64_t since = 0;
 #pragma unroll 1
       while (alive && oi < g.tiles) {
         const uint32_t sg = uniform(si % kGroups), og = uniform(oi % kGroups);
@@ -211,11 +210,10 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
         const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity & 1));
         const bool do_s = (yes & 3u) == 3u && si < g.tiles, do_o = (yes & 12u) == 12u && oi < si;
         if (!do_s && !do_o) {
-          if (++spin < (1u << 23)) continue;
-          alive = false;
-          *dead = 1;
-          if (lane == 0) atomicOr(p.err, kFlagTimeout);
-          break;
+          if ((++spin & (kAttempts - 1)) != 0) continue;
+          if (spin == kAttempts) since = global_timer_ns();
+          alive = all(keep_waiting(waits, since));
+          continue;
         }
         spin = 0;
         tc_fence_after();
