@@ -250,6 +250,7 @@ class TreeStep:
         dev = lengths.device
         bf16, i32 = torch.bfloat16, torch.int32
         self.workspace = ffd.tree_workspace(shape, n, device=dev)
+        self._flags = self.workspace[:4].view(i32)  # what ffd_check_device_status reads
         self.q, self.out, self._rotated = (torch.zeros((B, n, Hq, 128), dtype=bf16, device=dev) for _ in range(3))
         self.k_new, self.v_new = (torch.zeros((B, n, Hkv, 128), dtype=bf16, device=dev) for _ in range(2))
         mask, depth = ffd.tree_from_parents([list(range(-1, n - 1))] * B)
@@ -292,12 +293,31 @@ class TreeStep:
         (int64 [B, m] and int32 [B], on the device; the rest of a row is
         ignored): node i of the list becomes token lengths[b] + i, rotated for
         that position, and ``lengths`` grows by counts.  The list is a path of the
-        tree from a root, so its keys are the ones already attended to."""
-        torch, B, m = self.torch, self.shape.batch, nodes.shape[1]
-        at = nodes.clamp(0, self.k_new.shape[1] - 1)[:, :, None, None].expand(B, m, self.shape.num_kv_heads, 128)
-        self.lengths.add_(counts)
+        tree from a root, so its keys are the ones already attended to.  A sequence
+        whose count is outside [0, m], that has no room for it, or whose list names a
+        node outside [0, sizes[b]) stays as it is, and FFD_DEVICE_FLAG_BAD_LENGTH is
+        raised (:meth:`check`)."""
+        torch, B, n = self.torch, self.shape.batch, self.k_new.shape[1]
+        dev = self.lengths.get_device()
+        if nodes.dim() != 2:
+            raise ValueError(f"nodes: want int64 [B, m], got {tuple(nodes.shape)}")
+        m = nodes.shape[1]
+        ffd._tensor(counts, torch.int32, (B,), "counts", dev)
+        if nodes.dtype is not torch.int64 or nodes.shape[0] != B or nodes.get_device() != dev:
+            raise ValueError(f"nodes: want int64 [{B}, m] on cuda:{dev}, got {nodes.dtype} {tuple(nodes.shape)} "
+                             f"on {nodes.device}")
+        if m > self.shape.capacity:
+            raise ValueError(f"nodes: {m} a sequence are more than the cache holds")
+        listed = torch.arange(m, device=nodes.device) < counts[:, None]
+        known = (nodes >= 0) & (nodes < self.sizes[:, None])
+        good = ((known | ~listed).all(1) & (counts >= 0) & (counts <= m) & (self.lengths >= 0) &
+                (self.lengths <= self.shape.capacity - counts))
+        self._flags.bitwise_or_((~good).any().to(torch.int32) * ffd.FFD_DEVICE_FLAG_BAD_LENGTH)
+        kept = torch.where(good, counts, 0)
+        at = nodes.clamp(0, n - 1)[:, :, None, None].expand(B, m, self.shape.num_kv_heads, 128)
+        self.lengths.add_(kept)
         ffd.append_tokens(self.shape, self.cache, self.k_new.gather(1, at), self.v_new.gather(1, at), self.lengths,
-                          rope=self.rope, new_lengths=counts)
+                          rope=self.rope, new_lengths=kept)
 
     def check(self) -> int:
         """Device flags (ffd.FFD_DEVICE_FLAG_*) raised since the last check."""
