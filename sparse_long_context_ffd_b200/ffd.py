@@ -598,6 +598,8 @@ def append_tokens(shape: Shape, cache: KVCache, k_new, v_new, lengths, rope: Opt
     counted; new_lengths int32 [B] for fewer than n; positions int32 [B, n]
     (default: the slots)."""
     e, dev = _entry(), cache.device
+    if k_new.dim() != 4:
+        raise ValueError("k_new is [B, n, Hkv, 128]")
     bf16, i32, B, n = e.bf16, e.i32, shape.batch, k_new.shape[1]
     kv = (B, n, shape.num_kv_heads, 128)
     if (q is None) != (q_out is None):
@@ -619,7 +621,10 @@ def read_cache(shape: Shape, cache: KVCache, lengths, token_begin: int, k_out=No
     if k_out is None and v_out is None:
         raise ValueError("nothing to read: k_out and v_out are None")
     e, dev = _entry(), cache.device
-    count = (k_out if k_out is not None else v_out).shape[2]
+    what, out = ("k_out", k_out) if k_out is not None else ("v_out", v_out)
+    if out.dim() != 4:
+        raise ValueError(f"{what} is [B, Hkv, count, 128]")
+    count = out.shape[2]
     want = (shape.batch, shape.num_kv_heads, count, 128)
     _call(dev, stream, "ffd_read_cache", e.read_cache, shape, cache._of(shape),
           _tensor(lengths, e.i32, (shape.batch,), "lengths", dev), int(token_begin), count,
@@ -652,6 +657,8 @@ def decode_tree(shape: Shape, cache: KVCache, q, lengths, out, workspace, tree_m
     word: i sees j; default a chain); tree_sizes int32 [B] for fewer than n
     nodes.  tree_from_parents makes masks from parent lists."""
     e, dev = _entry(), cache.device
+    if q.dim() != 4:
+        raise ValueError("q is [B, n, Hq, 128]")
     B, n = shape.batch, q.shape[1]
     qs = (B, n, shape.num_q_heads, 128)
     if workspace.dim() != 1 or workspace.element_size() != 1:

@@ -249,6 +249,8 @@ class TreeStep:
         B, Hq, Hkv, n = shape.batch, shape.num_q_heads, shape.num_kv_heads, int(num_nodes)
         dev = lengths.device
         bf16, i32 = torch.bfloat16, torch.int32
+        cache._of(shape)
+        ffd._tensor(lengths, i32, (B,), "lengths", cache.device)
         self.workspace = ffd.tree_workspace(shape, n, device=dev)
         self._flags = self.workspace[:4].view(i32)  # what ffd_check_device_status reads
         self.q, self.out, self._rotated = (torch.zeros((B, n, Hq, 128), dtype=bf16, device=dev) for _ in range(3))
