@@ -686,7 +686,10 @@ __global__ void __launch_bounds__(128) merge_tree_kernel(const TreeParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t *out = p.out + static_cast<size_t>(blockIdx.x) * kHeadDim;
   asm volatile("griddepcontrol.launch_dependents;");
-  const Sequence q(p, b);  // (an input, not something the kernel before leaves)
+  // (lengths and sizes are inputs, and the call's kernel before has waited for what
+  // wrote them; with an empty cache there is none)
+  if (p.ctas == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Sequence q(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!q.good) {
     if (threadIdx.x == 0 && i == 0 && head == 0) atomicOr(p.err, kFlagBadLength);
