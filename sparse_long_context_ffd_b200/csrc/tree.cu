@@ -90,7 +90,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
   uint64_t *bar_end = bar_s + 7;
   Waits *waits = reinterpret_cast<Waits *>(smem + L::kWords + 32);
   volatile int *words = reinterpret_cast<volatile int *>(smem + L::kWords);
-  volatile int *odd = words + 1;       // a value in a drafted token's row is not finite
+  // The last segment with a drafted token's value that is not finite.  (Not a flag
+  // to be cleared: the groups go on to a next segment without waiting for each other.)
+  volatile int *odd = words + 1;
   int *start_s = const_cast<int *>(words) + 2;  // b, offset, tiles, all tiles
 
   if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t *>(smem + L::kWords), 512);
@@ -273,8 +275,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     const uint32_t tm_s = tmem + lanes + 128 * s, tm_o = tmem + lanes + 256 + 128 * s;
     uint32_t s_count = 0, o_count = 0, n = 0;
     uint32_t queries = 0;                        // tiles of query rows asked for (bf16; thread 0)
-    bool starts = true;                          // the CTA's first segment
+    int segment = 0;                             // of the CTA, from 1
     while (walk.next(p, g)) {
+      ++segment;
+      const bool starts = segment == 1;
       const int head = g.unit / p.units_a_head;
       const int block = (g.unit - head * p.units_a_head) * kTreeRows + (kPair ? s * kGroup : 0);
       const int first = g.len - g.size;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
               vs = 0.0f;
             } else if (!(fabsf(vs) < INFINITY)) {
               vs = 0.0f;
-              *odd = 1;
+              *odd = segment;
             }
           }
           mine[t] = bf16_f(raw[t]);
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
           wait(full + v_slot, (vi / kSlots) & 1);
           if (t0 + t >= first &&
               clean_values<kByte>(smem + L::kRing + v_slot * L::kSlot, t, t0 + t >= g.len, 0, kByte ? 8 : 16))
-            *odd = 1;
+            *odd = segment;
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       if (!kPair || (g.tile0 + g.tiles) * kTile > first) named_barrier(1, 2 * kGroup);
       else named_barrier(2 + s, kGroup);
       const bool whole = g.tiles == g.all;
-      const bool any_odd = *odd != 0;
+      const bool any_odd = *odd == segment;
       float f0 = 1.0f, f1 = 0.0f, row_m = m, row_l = l;
       if constexpr (!kPair) {
         row_m = -INFINITY;
@@ -653,11 +657,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
       }
       if (t == 0) bulk_wait_read<0>();
       if (tid == 0 && g.tile0 == 0) note_unit(p, g, walk, start_s, starts);
-      starts = false;
       tc_fence_before();
       fence_proxy_async_smem();  // the next Q comes over what was staged
       named_barrier(1, 2 * kGroup);
-      if (tid == 0) *odd = 0;
     }
     if (t == 0) bulk_wait<0>();
     // (the products waited for them, but may have been given up)
