@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         uint64_t *bar = (lane & 1) ? full + v_slot : (lane & 2) ? bar_p + og : full + k_slot;
         const uint32_t parity = (lane & 1) ? va / kSlots : (lane & 2) ? p_phases >> og : ka / kSlots;
         const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity & 1));
+        __syncwarp();  // (what the asking lanes have seen, the issuing one has)
         const bool do_o = (yes & 6u) == 6u && oi < si;
         const bool do_s = (yes & 1u) != 0 && si < items && si < oi + (do_o ? 3 : 2);
         if (!do_s && !do_o) {

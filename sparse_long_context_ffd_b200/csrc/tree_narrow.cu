@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
         uint64_t *bar = (lane & 2) ? ((lane & 1) ? bar_p + og : full + v_slot) : ((lane & 1) ? bar_f + sg : full + k_slot);
         const uint32_t parity = (lane & 2) ? ((lane & 1) ? p_phases >> og : va / kSlots) : ((lane & 1) ? f_phases >> sg : ka / kSlots);
         const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity & 1));
+        __syncwarp();  // (what the asking lanes have seen, the issuing one has)
         const bool do_s = (yes & 3u) == 3u && si < g.tiles, do_o = (yes & 12u) == 12u && oi < si;
         if (!do_s && !do_o) {
           if ((++spin & (kAttempts - 1)) != 0) continue;
@@ -322,11 +323,14 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
         const int t0 = (g.tile0 + j) * kTile, token = t0 + t;
         const bool masked = t0 + kTile > first;
         const uint32_t vi = 2 * (n + j) + 1, v_slot = vi % kSlots, k_slot = (vi - 1) % kSlots;
-        wait(bar_s + s, count & 1);
-        tc_fence_after();
         float ks = kScoreScale, vs = 1.0f, lv = 0.0f;
         if constexpr (kByte) {
+          wait(full + k_slot, ((vi - 1) / kSlots) & 1);
           ks = bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + k_slot * 256)[t]);
+        }
+        wait(bar_s + s, count & 1);
+        tc_fence_after();
+        if constexpr (kByte) {
           wait(full + v_slot, (vi / kSlots) & 1);
           vs = bf16_f(reinterpret_cast<const uint16_t *>(smem + L::kScales + v_slot * 256)[t]);
           if (masked && token >= first) {
