@@ -442,9 +442,12 @@ ffd_status ffd_read_probe(const void *buf, size_t bytes, uint32_t *sink, void *c
  *   FFD_ROPE_SCALE_BY_PARTS  with r = original_length * f_i / (2 pi) rotations
  *                            over the trained length and g = clamp((r - low) /
  *                            (high - low), 0, 1): (1 - g) f_i / factor + g f_i
- * Angles are exact to 2^-32 of a turn at any 32-bit position, negative ones
- * included: the frequency is held in turns as a 64-bit binary fraction, so the
- * product with the position wraps at whole turns. */
+ * The ramp of the last one runs linearly over the rotations.  Where a model's runs
+ * linearly over the pair index instead, between the pairs at which r is high and
+ * low, its frequencies differ: write them to `turns` after ffd_rope_init.
+ * Frequencies are held in turns as 64-bit binary fractions, so that the product with
+ * a position wraps at whole turns: the angle is off by at most 2^-26 of a turn (half
+ * a step of fp32 at half a turn) at any 32-bit position, negative ones included. */
 #define FFD_ROPE_HALF 0
 #define FFD_ROPE_INTERLEAVED 1
 #define FFD_ROPE_SCALE_NONE 0
@@ -467,7 +470,7 @@ typedef struct {
 /* A rotary plan: host memory, filled by ffd_rope_init and read by the calls
  * below before they return. */
 typedef struct {
-  uint64_t turns[64];     /* per pair: f_i / (2 pi) as a 64-bit binary fraction */
+  uint64_t turns[64];     /* per pair: the fraction of f_i / (2 pi), times 2^64 */
   float amplitude;
   int32_t rotary_dim, layout, reserved;
 } ffd_rope;
@@ -493,7 +496,8 @@ ffd_status ffd_rotate(const ffd_rope *rope, int64_t tokens, const int32_t *d_pos
  *       amax = max_c |x_c|,  s = bf16_rne(amax / 448)   (IEEE fp32 division)
  *       code_c = s == 0 ? 0 : e4m3_rne(x_c / s), clamped to +-448
  *     and stands for code_c * s.  A row with an infinity or NaN in it gets a
- *     NaN scale and NaN codes: it reads back as NaN throughout. */
+ *     NaN scale and NaN codes: it reads back as NaN throughout.  Scales that
+ *     come from elsewhere are not negative, and finite or NaN, too. */
 #define FFD_CACHE_BF16 0
 #define FFD_CACHE_BYTE 1
 
@@ -515,7 +519,11 @@ typedef struct {
  *     each token's slot).
  * Token i of sequence b goes to slot lengths[b] - count + i, k rotated in fp32
  * and rounded (or quantised) once.  Rows i >= count of q_out and every other
- * row of the cache are left as they were.  A sequence whose length is outside
+ * row of the cache are left as they were.  Rows written to a cache of ffd_decode
+ * leave its low-bit keys behind: several rows may end one block and begin others,
+ * so quantise again from the first block that changed, ffd_quantize_keys (_tr) with
+ * block_begin = (the shortest sequence's length before) / T.  FFD_LAST_BLOCK and
+ * ffd_decode_append refresh the last block alone.  A sequence whose length is outside
  * [0, cap], or whose count is outside [0, min(new_tokens, length)], is left
  * out (ffd_decode_tree reports it).  q_out may be q; other overlaps between
  * inputs and outputs are rejected. */
@@ -550,12 +558,14 @@ ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const 
  * With first = lengths[b] - size, node i of head h attends (softmax(q.K /
  * sqrt(D)) V with the head's kv-head) over slots 0 .. first - 1 and the slots
  * first + j it sees, j < size.  A node that sees nothing yields a zero row;
- * what lies in unseen slots, NaN included, has no influence.  Rows i >= size
+ * what lies in unseen slots, NaN included, has no influence (an infinity in a seen
+ * value before the tree may come out as NaN).  Rows i >= size
  * of out are left as they were.  Scores, softmax statistics and sums are fp32;
  * the softmax weights enter the product with V with 8 significant bits.  Over an
  * FFD_CACHE_BYTE cache so do the weights times V's scales, in units no coarser
- * than 2^-16 of the largest one met so far, and the queries, in units no coarser
- * than 2^-16 of the largest magnitude in the row.
+ * than 2^-16 of the largest one met so far (scales below 2^-60 count as 2^-60
+ * there), and the queries, in units no coarser than 2^-16 of the largest magnitude in
+ * the row.
  * A row whose scores pass 2^29 in magnitude (over an FFD_CACHE_BYTE cache 2^18),
  * more than fp32 tells apart well enough, may be NaN.
  * A sequence whose length is outside [0, cap], or whose size is outside [0,

@@ -596,7 +596,8 @@ def append_tokens(shape: Shape, cache: KVCache, k_new, v_new, lengths, rope: Opt
     write the new K/V rows into the cache.  k_new, v_new bf16 [B, n, Hkv, 128];
     q, q_out bf16 [B, n, Hq, 128] or neither; lengths int32 [B], the new tokens
     counted; new_lengths int32 [B] for fewer than n; positions int32 [B, n]
-    (default: the slots)."""
+    (default: the slots).  For ffd.decode on the same cache, quantize_keys again from
+    the first block that changed on."""
     e, dev = _entry(), cache.device
     if k_new.dim() != 4:
         raise ValueError("k_new is [B, n, Hkv, 128]")

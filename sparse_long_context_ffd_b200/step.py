@@ -295,7 +295,9 @@ class TreeStep:
         (int64 [B, m] and int32 [B], on the device; the rest of a row is
         ignored): node i of the list becomes token lengths[b] + i, rotated for
         that position, and ``lengths`` grows by counts.  The list is a path of the
-        tree from a root, so its keys are the ones already attended to.  A sequence
+        tree from a root, so its keys are the ones already attended to.  (The low-bit
+        keys of ffd.decode on the same cache are the caller's: quantize_keys from the
+        first block that changed on.)  A sequence
         whose count is outside [0, m], that has no room for it, or whose list names a
         node outside [0, sizes[b]) stays as it is, and FFD_DEVICE_FLAG_BAD_LENGTH is
         raised (:meth:`check`)."""
