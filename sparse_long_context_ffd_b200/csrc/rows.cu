@@ -55,7 +55,8 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
 // The angles come first: thread t finds (cos, sin) of one pair of one token
 // and leaves them in shared memory, since every head of the token needs them.
 // position * turns wraps at whole turns in 64 bits; its top 32 bits, signed,
-// are the angle in turns to 2^-32, and sincospif takes it from there.  Where a
+// are the angle in turns to 2^-32, which fp32 rounds by up to 2^-26 of a turn, and
+// sincospif takes it from there.  Where a
 // row comes from and goes to is found by one thread instead of 16.
 //
 // Then 16 threads take rows of one token, kInFlight before the first is used (a
