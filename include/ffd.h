@@ -152,6 +152,8 @@ ffd_status ffd_quantize_keys(const ffd_shape *shape, const void *k_bf16,
  *   flash-decoding over all valid tokens (k_packed, k_scales may be NULL).
  *
  * A sequence with lengths[b] == 0 yields zero output rows and an empty mask.
+ * Tokens at or past lengths[b] have no influence, as long as their values (v) are
+ * finite: weights of zero meet them.
  * lengths[b] outside [0, cap] sets FFD_DEVICE_FLAG_BAD_LENGTH in the
  * workspace and yields zero rows and an empty mask for that sequence.
  * Steps that share a workspace must not overlap on the GPU. */
@@ -537,8 +539,9 @@ ffd_status ffd_append_tokens(const ffd_shape *shape, const ffd_cache *cache, con
  * FFD_CACHE_BYTE cache back to bf16: k_out, v_out [B][Hkv][token_count][D],
  * code * scale rounded once (either may be NULL).  With token_begin 0 and
  * token_count cap the outputs are a cache for ffd_quantize_keys and
- * ffd_decode.  Rows of tokens at or past lengths[b] are left as they were, as
- * is a sequence whose length is outside [0, cap].  0 <= token_begin,
+ * ffd_decode, whose v_out must be finite past the lengths before the call.  Rows
+ * of tokens at or past lengths[b] are left as they were, as is a sequence whose
+ * length is outside [0, cap].  0 <= token_begin,
  * 0 <= token_count, token_begin + token_count <= cap. */
 ffd_status ffd_read_cache(const ffd_shape *shape, const ffd_cache *cache, const int32_t *d_lengths,
                           int32_t token_begin, int32_t token_count, void *k_out_bf16,

@@ -530,7 +530,7 @@ def _call(device: int, stream, what: str, fn, *args) -> None:
 class KVCache:
     """A KV cache of one layer: bf16 k and v [B, Hkv, cap, 128], or
     float8_e4m3fn k and v with bf16 k_scales and v_scales [B, Hkv, cap] (one
-    scale a row).  Wraps the caller's tensors; `KVCache.empty` allocates."""
+    scale a row).  Wraps the caller's tensors; `KVCache.empty` makes new ones."""
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         import torch
@@ -550,15 +550,17 @@ class KVCache:
 
     @classmethod
     def empty(cls, shape: Shape, format: int = FFD_CACHE_BF16, device="cuda"):
+        """A cache without tokens, all zero: ffd_decode wants finite values past a
+        sequence's length."""
         import torch
         key = (shape.batch, shape.num_kv_heads, shape.capacity)
         if format == FFD_CACHE_BF16:
-            kv = [torch.empty((*key, 128), dtype=torch.bfloat16, device=device) for _ in range(2)]
+            kv = [torch.zeros((*key, 128), dtype=torch.bfloat16, device=device) for _ in range(2)]
             return cls(*kv)
         if format != FFD_CACHE_BYTE:
             raise ValueError("unknown cache format")
-        kv = [torch.empty((*key, 128), dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
-        return cls(*kv, *(torch.empty(key, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        kv = [torch.zeros((*key, 128), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(*kv, *(torch.zeros(key, dtype=torch.bfloat16, device=device) for _ in range(2)))
 
     def _of(self, shape: Shape):
         if self.key != (shape.batch, shape.num_kv_heads, shape.capacity):
