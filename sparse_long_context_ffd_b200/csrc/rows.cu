@@ -2,11 +2,13 @@
 // and the 8-bit cache read back.
 //
 // All three pass once over rows of 128 channels.  At small counts they are the
-// launch and the host's call (16 tokens: 6.8 us a call back to back; a kernel may
-// start while the one before it ends, 7.6 without).  At large ones rotation and
-// read-back are near HBM's rate (8191 tokens x 40 heads: 32 us, 5.3 TB/s; read-back
-// 5.5 to 5.8), and the 8-bit write is bound by instruction issue (32K tokens: 173
-// us, 4.3 TB/s, 65% of issue slots taken).
+// launch and the host's call (16 tokens: 7 us a call back to back; a kernel may start
+// while the one before it ends, 0.8 us more without).  At large ones rotation and
+// read-back are near HBM's rate (8191 tokens x 40 heads, half of the channels,
+// interleaved: 32 us, 5.3 TB/s, all of them in halves: 38; read-back 5.4 to 5.8), as is
+// the bf16 write (32K tokens: 150 us, 5.4 TB/s).  The 8-bit write is slowed by
+// instruction issue (173 us, 4.3 TB/s, 65% of issue slots taken): each of a row's 16
+// threads does the row's division and reciprocal again.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -56,8 +58,8 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
 // and leaves them in shared memory, since every head of the token needs them.
 // position * turns wraps at whole turns in 64 bits; its top 32 bits, signed,
 // are the angle in turns to 2^-32, which fp32 rounds by up to 2^-26 of a turn, and
-// sincospif takes it from there.  Where a
-// row comes from and goes to is found by one thread instead of 16.
+// sincospif takes it from there.  Where a row comes from and goes to is found by one
+// thread instead of 16.
 //
 // Then 16 threads take rows of one token, kInFlight before the first is used (a
 // block has 16 KB on its way from HBM), each with the angles of its channels in
@@ -65,7 +67,6 @@ __device__ __forceinline__ int token_slot(const RowsParams &p, int b, int i) {
 // bandwidth and set the pace.  Where the pairs' halves fall on whole
 // threads (rotary_dim a multiple of 16, or interleaved) the partner channels
 // come by shuffle; else each partner is loaded on its own.
-//
 constexpr int kInFlight = 4;
 constexpr int kTableRows = kThreads;
 
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, kByte ? 4 : 5) rows_kernel(const __g
 
   const int lane = threadIdx.x & (kRowLanes - 1);
   const int c0 = 8 * lane;
-  const int mine_token = (threadIdx.x / kRowLanes) % tokens_a_block;  // tokens_a_block: a power of two up to 16
+  const int mine_token = (threadIdx.x / kRowLanes) % tokens_a_block;  // tokens_a_block: a power of two up to 8
   const int first_row = threadIdx.x / kRowLanes / tokens_a_block, row_step = kRowsAtOnce / tokens_a_block;
   const float2 *cs = turn_s + mine_token * half;
   // the pairs of this thread's channels: 8 of them, or (interleaved) 4
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, kByte ? 4 : 5) rows_kernel(const __g
 
 // Sixteen codes (16 bytes in, 32 out) a thread; code * scale is exact in fp32 (4
 // and 8 significant bits), so the only rounding is the one to bf16.  Bound by HBM
-// (4 x 8 x 32768 tokens: 140 to 146 us, 5.5 to 5.8 TB/s; 18 MB: 5.8 us).  One row a thread and
+// (4 x 8 x 32768 tokens: 139 to 149 us, 5.4 to 5.8 TB/s; 18 MB: 5.8 us).  One row a thread and
 // more blocks beat several rows in flight a thread: 2, 4 and 8 of them took 141,
 // 144 and 154 us, and of the 18 MB 8.1, 8.2 and 9.0 us where one took 7.2.
 constexpr int kReadLanes = 8;  // threads of a row

@@ -18,17 +18,20 @@
 // of the same tiles.  Either way the tensor cores work for one group while the
 // other does its exponentials.
 //
-// What bounds it: a group's chain of a tile.  With 2 x 128 rows (64 nodes, 3
-// sequences of up to 16K tokens, 58 us) it is 1600 clocks of exponentials, two
-// products of 512 each that wait 300 to 700 for the other group's, and 300 until
-// the answer is seen: 4300 for a pair of tiles, of which the tensor cores work
-// 2048.  With 64 rows over bf16 (16 nodes, 128K tokens, 103 us, 5.2 TB/s) the
-// tiles come at 85% of the copy's rate in between, and the start, the last parts
-// and the merge take 13 us.  Over e4m3 (13 nodes, 5 sequences of up to 64K, 143 us)
-// the two parts of queries and weights make two products of each, at half the
-// bytes: the chain, 3000 clocks a tile, sets the pace.  One matrix warp for each
-// group, as they please or under a lock, was slower (both groups fall into step:
-// 74 and 69 us where one warp took 67), and so were two threads a row (95 us).
+// What bounds it.  A tile's time is the difference between 32 tiles a CTA and 8,
+// every multiprocessor busy.  64 rows over bf16: 1.3 us (2200 clocks), 7.4 TB/s, the
+// copies.  52 rows over e4m3 (13 nodes, group 4): 2250 clocks, where the bytes would
+// take 1290 at the copies' rate; a group, which has every other tile, needs twice that
+// for its chain of scales, maxima, exponentials and the split of each weight, and two
+// products of each kind in turn with the other group's.  2 x 128 rows: 3600 a pair of
+// tiles, of which the tensor cores work 2048, and 7900 over e4m3.  The rest of a call is
+// its start, the parts and the merge: of 16 nodes over 128K tokens (104 us) 74 are
+// the 56 tiles of a CTA, of 64 nodes over 3 sequences of up to 16K (58 us) 26 are its
+// 14 pairs, of 13 nodes over 5 sequences of up to 64K in e4m3 (144 us) 95.  Up to 19
+// MB of parts go out and come back, and a merge CTA starts for every row, also where
+// no unit was cut (1.1 us a thousand).  One matrix warp for each group, as they please
+// or under a lock, was slower (both groups fall into step: 74 and 69 us where one warp
+// took 67), and so were two threads a row (95 us).
 //
 // bf16 cache: P has bf16's 8 significant bits.  8-bit cache: codes enter the
 // matrix instructions as they are.  The query row, scaled by a power of two
@@ -150,45 +153,42 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     }
   };
 
-  if (warp >= 8) {
-    if (warp == 8) {
+  if (warp == 8) {
     // ------------------------------------------------------------- copies --
     // (the whole warp walks and waits, one lane issues)
-    {
-      uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
-      while (alive && walk.next(p, g)) {
-        if (!kByte && i == 0 && elect_one()) load_query(g);
-        __syncwarp();
-        const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
-        for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
-          const uint32_t slot = i % kSlots, round = i / kSlots;
-          // (a slot given back by a thread that waits no more may still be filling)
-          if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1) && waits->dead == 0);
-          if (!alive) break;
-          const int t0 = (g.tile0 + (j >> 1)) * kTile;
-          const int row = bh * p.capacity + t0;
-          uint64_t *landed = full + slot;
-          uint8_t *dst = smem + L::kRing + slot * L::kSlot;
-          const void *map = (j & 1) ? &tmap_v : &tmap_k;
-          if (!elect_one()) continue;
-          if constexpr (kByte) {
-            const uint32_t scale_bytes = 2u * static_cast<uint32_t>(min(kTile, p.capacity - t0));
-            mbar_arrive_expect_tx(landed, L::kSlot + ((j & 1) ? 2 * scale_bytes : 0));
-            tma_load_2d(dst, map, 0, row, landed);
-            if (j & 1) {
-              bulk_g2s(smem + L::kScales + slot * 512, p.k_scales + row, scale_bytes, landed);
-              bulk_g2s(smem + L::kScales + slot * 512 + 256, p.v_scales + row, scale_bytes, landed);
-            }
-          } else {
-            mbar_arrive_expect_tx(landed, L::kSlot);
-            tma_load_3d(dst, map, 0, row, 0, landed);
+    uint32_t i = 0;  // K of tile n is copy 2n, V copy 2n + 1
+    while (alive && walk.next(p, g)) {
+      if (!kByte && i == 0 && elect_one()) load_query(g);
+      __syncwarp();
+      const int bh = g.b * p.kv_heads + g.unit / p.units_a_head;
+      for (int j = 0; alive && j < 2 * g.tiles; ++j, ++i) {
+        const uint32_t slot = i % kSlots, round = i / kSlots;
+        // (a slot given back by a thread that waits no more may still be filling)
+        if (round > 0) alive = all(wait(empty + slot, (round - 1) & 1) && waits->dead == 0);
+        if (!alive) break;
+        const int t0 = (g.tile0 + (j >> 1)) * kTile;
+        const int row = bh * p.capacity + t0;
+        uint64_t *landed = full + slot;
+        uint8_t *dst = smem + L::kRing + slot * L::kSlot;
+        const void *map = (j & 1) ? &tmap_v : &tmap_k;
+        if (!elect_one()) continue;
+        if constexpr (kByte) {
+          const uint32_t scale_bytes = 2u * static_cast<uint32_t>(min(kTile, p.capacity - t0));
+          mbar_arrive_expect_tx(landed, L::kSlot + ((j & 1) ? 2 * scale_bytes : 0));
+          tma_load_2d(dst, map, 0, row, landed);
+          if (j & 1) {
+            bulk_g2s(smem + L::kScales + slot * 512, p.k_scales + row, scale_bytes, landed);
+            bulk_g2s(smem + L::kScales + slot * 512 + 256, p.v_scales + row, scale_bytes, landed);
           }
+        } else {
+          mbar_arrive_expect_tx(landed, L::kSlot);
+          tma_load_3d(dst, map, 0, row, 0, landed);
         }
       }
-      // what is in flight lands before the CTA ends, whoever gave up
-        for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
-          mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
     }
+    // what is in flight lands before the CTA ends, whoever gave up
+    for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
+      mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
   } else if (warp == 9) {
     // ------------------------------------------------------------ matrices --
     // Item i of a segment is a tile's product pair for group i % 2.  S goes out
@@ -264,8 +264,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     if (elect_one()) mma_commit(bar_end);
     __syncwarp();
     mbar_wait(bar_end, 0, kWaitLimitNs);
-    }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------- softmax --
     const int s = warp >> 2;                     // group
     const int t = tid & (kGroup - 1);            // lane of the accumulator

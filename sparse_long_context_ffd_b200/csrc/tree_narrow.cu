@@ -13,12 +13,12 @@
 //
 // Groups of 128 threads take the tiles in turn, with an S and an O each.
 //
-// One token of 4 sequences x 32K over e4m3 (4 rows): 60 us, 4.5 TB/s, where the
-// kernel with rows as lanes took 80; the issue of the products (about 900 clocks a
-// tile, of which they run 320) sets the pace against 1290 that the bytes take at
-// the copy's rate, and the start and the merge add 10 us.  With 32 and 64 rows
-// this form was slower than the other (190 us where it took 146: every weight of
-// every column passes one thread's arithmetic).
+// One token of 4 sequences x 32K over e4m3 (4 rows): 62 us, 4.4 TB/s, where the
+// kernel with rows as lanes took 80.  48 of them are the tiles, 64 in each of the 128
+// CTAs that the 32 units are cut for, at 0.75 us (1340 clocks, 5.7 TB/s); start, parts
+// and merge take the others.  With 32 and 64 rows this form was slower than the other
+// (190 us where it took 146: every weight of every column passes one thread's
+// arithmetic).
 #include <atomic>
 
 #include "ffd_tree.cuh"
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(Narrow<kByte>::kThreads, 1)
     }
     __syncwarp();
     // what is in flight lands before the CTA ends, whoever gave up
-      for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
-        mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
+    for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < i; ++s)
+      mbar_wait(full + s, ((i - 1 - s) / kSlots) & 1, kWaitLimitNs);
   } else if (warp == kMatrixWarp) {
     // ------------------------------------------------------------ matrices --
     // Tile i of a segment is group i % kGroups'.  S of a tile goes out when its K
